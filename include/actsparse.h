@@ -21,8 +21,8 @@
  *     stream).  Scratch memory is passed in as `workspace`, sized with
  *     as_workspace_size().  Workspace must be zero-filled once before its
  *     first use; every call leaves it zero-filled again.  The exceptions
- *     are as_weight_prep_amber, as_rsparse_decode, as_linear_prefill_hybrid
- *     and as_block_sparsity: they need no zero-fill and leave their
+ *     are as_weight_prep_amber, as_rsparse_decode, as_linear_prefill_hybrid,
+ *     as_block_sparsity and as_linear_decode_fp4: they need no zero-fill and leave their
  *     workspace in an unspecified state (do not share it with the other
  *     calls).  Calls that share a workspace must not run concurrently.
  *   - Errors are returned, never raised: arguments are validated on the host
@@ -322,7 +322,14 @@ as_status as_linear_decode_noalloc(const void *x, as_dtype dt, int T, int K, int
                                    float *eta_out, float *colnorm_out, cudaStream_t stream);
 
 /* Which operation a workspace size is asked for. */
-enum { AS_OP_WEIGHT_PREP = 0, AS_OP_SELECT = 1, AS_OP_DECODE = 2, AS_OP_PREFILL = 3, AS_OP_AMBER = 4 };
+enum {
+    AS_OP_WEIGHT_PREP = 0,
+    AS_OP_SELECT = 1,
+    AS_OP_DECODE = 2,
+    AS_OP_PREFILL = 3,
+    AS_OP_AMBER = 4,
+    AS_OP_DECODE_FP4 = 5
+};
 
 /* Bytes of workspace the operation needs (0 if none); (size_t)-1 if the
  * arguments are invalid. */
@@ -509,6 +516,128 @@ as_status as_select_sqrelu24_fp8(const void *z, int T, int K, uint8_t *x8, uint3
 as_status as_linear_prefill_fp8(const uint8_t *x8, const uint32_t *meta8, const float *x_scale, int T, int K,
                                 int n_out, const uint8_t *Wq, const float *w_scale, as_dtype out_dtype, void *y,
                                 cudaStream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Microscaled 4-bit weights and activations.  A value is an E2M1 code
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign; round to nearest, ties to the even
+ * code, saturating) times the scale of its block of B consecutive channels,
+ * times an optional float32 scale of its row:
+ *   AS_FP4_MX: B = 32, E8M0 scale s = 2^(byte - 127).  Quantiser:
+ *              s = 2^max(floor(log2 amax) - 2, -127), amax the block's largest
+ *              |v| (values between 6 s and 8 s saturate); 1 for a zero block.
+ *   AS_FP4_NV: B = 16, E4M3 scale s.  Quantiser: row scale S = 2^e with the
+ *              smallest e >= -126 for which amax_row <= 2688 * 2^e (2688 =
+ *              6 * 448; 1 for a zero row), s = E4M3(amax / (6 S)) rounded to
+ *              nearest even.  S is a power of two, so that s * S and every
+ *              border between two codes are exact in float32 and the codes
+ *              are those of the exact quotient v / (s S).
+ * A block that holds a NaN or an infinity gets the NaN scale (0xFF, 0x7F)
+ * and zero codes: everything that reads it is NaN.  It does not enter
+ * amax_row.
+ *   codes  [rows, K/2] bytes, channel 2i in the low and 2i + 1 in the high
+ *          four bits of byte i (bit 3 of a code is the sign).
+ *   sf     the blocks' scale bytes, as_fp4_sf_bytes(rows, K, fmt) bytes in
+ *          tiles of 128 rows x 4 blocks: tile (r, c) starts at byte
+ *          (r * ceil(K / (4 B)) + c) * 512 and holds row p, block j of the
+ *          tile at byte 16*(p % 32) + 4*(p / 32) + j (the order that the
+ *          tensor core reads scales in).  Bytes past rows or K are zero.
+ * K % 32 == 0, K <= 131072; pointers 16-byte aligned.  No workspace.
+ * ------------------------------------------------------------------------ */
+typedef enum as_fp4 { AS_FP4_MX = 0, AS_FP4_NV = 1 } as_fp4;
+
+/* Bytes of the scale buffer of `rows` x K values; 0 if the arguments are
+ * invalid.  Host-only. */
+size_t as_fp4_sf_bytes(int rows, int K, as_fp4 fmt);
+
+/* x [rows, K] in `dt` -> codes, sf and row_scale [rows] (required for
+ * AS_FP4_NV; optional for AS_FP4_MX, which writes ones). */
+as_status as_quant_fp4(const void *x, as_dtype dt, int rows, int K, as_fp4 fmt, uint8_t *codes, uint8_t *sf,
+                       float *row_scale, cudaStream_t stream);
+
+/* The values read back: out [rows, K] in `out_dtype` = code * s * row_scale
+ * (row_scale may be NULL: 1), exact in float32 for a power-of-two row scale,
+ * and rounded once to bf16. */
+as_status as_dequant_fp4(const uint8_t *codes, const uint8_t *sf, const float *row_scale, int rows, int K, as_fp4 fmt,
+                         as_dtype out_dtype, void *out, cudaStream_t stream);
+
+/* The product of two quantised operands on the block-scaled tensor cores
+ * (tcgen05.mma kind::mxf4nvf4, float32 accumulation in tensor memory):
+ *   y[t, o] = fl32(fl32(acc[t, o] * x_scale[t]) * w_scale[o]),
+ *   acc[t, o] = sum_i xq[t, i] * s_x * wq[o, i] * s_w  (values without the
+ *   row scales),
+ * rounded to out_dtype.  xq/x_sf: [T, K] activations, Wq/w_sf: [n_out, K]
+ * weights, both in `fmt`; x_scale [T] and w_scale [n_out] may be NULL (1).
+ * Any T >= 1: few tokens stream the weights with K split over a cluster,
+ * long prompts run 256 x 256 tiles on CTA pairs.  n_out % 8 == 0.
+ * Float32 accumulation in a fixed order (deterministic). */
+as_status as_linear_prefill_fp4(const uint8_t *xq, const uint8_t *x_sf, const float *x_scale, int T, int K, int n_out,
+                                const uint8_t *Wq, const uint8_t *w_sf, const float *w_scale, as_fp4 fmt,
+                                as_dtype out_dtype, void *y, cudaStream_t stream);
+
+/* Decode weights, once per layer: the quantised weight [n_out, K] re-laid so
+ * that a kept channel's codes are contiguous for 128 output columns.  Wd is
+ * opaque, as_fp4_decode_bytes(n_out, K, fmt) bytes, and carries w_scale
+ * (NULL: 1).  An output whose row holds a NaN scale gives NaN.  AS_FP4_MX
+ * weights below 2^-126 times the row's largest block scale may lose bits.
+ * as_fp4_decode_bytes is host-only and 0 if the arguments are invalid. */
+size_t as_fp4_decode_bytes(int n_out, int K, as_fp4 fmt);
+as_status as_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const float *w_scale, int n_out, int K,
+                             as_fp4 fmt, uint8_t *Wd, cudaStream_t stream);
+
+/* as_linear_decode on 4-bit weights: 1 <= T <= 16 tokens,
+ *   y = prune(x) W^T (+ eta_t rowsum_o with a token shift),
+ * W the values that Wq stands for.  Scores, selection, shift and the outputs
+ * mask_out, eta_out, colnorm_out are those of as_linear_decode; x is not
+ * quantised (the kept values enter the tensor cores as one to three bf16
+ * parts: exactly for float32 output, to 2^-17 for bf16 output).  g and rowsum
+ * describe the same W (as_weight_prep on its values).  Only the codes of
+ * channels that some token keeps are read.
+ *   x [T, K] in `dt`; K % 32 == 0, n_out % 8 == 0; cfg->var is not supported.
+ *   Workspace: as_workspace_size(AS_OP_DECODE_FP4, T, K, n_out, cfg); no
+ *   zero-fill needed, left in an unspecified state. */
+as_status as_linear_decode_fp4(const void *x, as_dtype dt, int T, int K, int n_out, const uint8_t *Wd, as_fp4 fmt,
+                               const float *g, const float *rowsum, const as_config *cfg, void *y,
+                               uint32_t *mask_out, float *eta_out, float *colnorm_out, void *workspace,
+                               size_t ws_bytes, cudaStream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Between two blocks: the norm after a block's output, its gate, the scaled
+ * residual and the norm before the next block, in one pass over the rows.
+ *   u_t  = y_t * rsqrt(mean(y_t^2) + eps) * (w_offset + post_w)  (post_norm;
+ *          u = y otherwise)
+ *   r'_t = res_scale * r_t + gate * u_t           (r_out, rounded to r_dtype)
+ *   h_t  = r'_t * rsqrt(mean(r'_t^2) + eps) * (w_offset + pre_w)
+ * h uses the float32 r', before it is rounded for storage.  All arithmetic is
+ * float32; the mean squares are sums of per-thread partials in a fixed order.
+ * With y == NULL only h = norm(r) is formed (r_out, gate, post_w NULL,
+ * post_norm 0; res_scale is not used).
+ *   r [T, D], y [T, D], h [T, D] each in its own dtype; post_w, pre_w [D]
+ *   float32 (NULL: the weight is 1 and w_offset is not added); gate float32,
+ *   [D] (gate_rows 1) or [T, D] (gate_rows T), NULL: 1.
+ *   r_out may be r (each row is read before it is written); no other output
+ *   may overlap an input.  r_out, h and the fp4 outputs are each optional.
+ *   h_q, h_sf, h_scale: h as the quantised operand of as_linear_prefill_fp4
+ *   (as as_quant_fp4 of the float32 h), needs D % 32 == 0; h_scale as there.
+ * D % 8 == 0, D <= 32768; pointers 16-byte aligned.  No workspace.
+ * ------------------------------------------------------------------------ */
+typedef struct as_norm_args {
+    const void *r;       /* [T, D] residual stream */
+    const void *y;       /* [T, D] block output, or NULL */
+    void *r_out;         /* [T, D] in r_dtype, optional */
+    void *h;             /* [T, D] in h_dtype, optional */
+    const float *post_w; /* [D] */
+    const float *pre_w;  /* [D] */
+    const float *gate;   /* [gate_rows, D] */
+    uint8_t *h_q;        /* fp4 operand of h, optional (with h_sf) */
+    uint8_t *h_sf;
+    float *h_scale;
+    int32_t r_dtype, y_dtype, h_dtype; /* as_dtype */
+    int32_t gate_rows;   /* 1 or T */
+    int32_t post_norm;   /* 0 or 1 */
+    int32_t fmt;         /* as_fp4 of h_q */
+    float res_scale, eps, w_offset;
+} as_norm_args;
+as_status as_norm_residual(const as_norm_args *a, int T, int D, cudaStream_t stream);
 
 /* Synchronises `stream`, then reports (and clears) a device-side error such
  * as AS_ERR_TIMEOUT recorded by a kernel of this library, or AS_ERR_CUDA if

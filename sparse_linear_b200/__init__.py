@@ -34,6 +34,8 @@ AS_SCORE_MAG, AS_SCORE_WEIGHT, AS_SCORE_CLACT = 0, 1, 2
 AS_SEL_NM, AS_SEL_TOPK, AS_SEL_ALL, AS_SEL_THRESH = 0, 1, 2, 3
 AS_PTS_OFF, AS_PTS_DYNAMIC, AS_PTS_STATIC = 0, 1, 2
 AS_OP_WEIGHT_PREP, AS_OP_SELECT, AS_OP_DECODE, AS_OP_PREFILL, AS_OP_AMBER = 0, 1, 2, 3, 4
+AS_OP_DECODE_FP4 = 5
+AS_FP4_MX, AS_FP4_NV = 0, 1
 AS_MAX_DECODE_T = 16
 AS_MODE_24, AS_MODE_SPLIT, AS_MODE_DENSE = 0, 1, 2
 
@@ -45,7 +47,9 @@ EXPORTS = [
     "as_linear_prefill_fp8", "as_rsparse_workspace", "as_rsparse_decode", "as_hybrid_workspace",
     "as_linear_prefill_hybrid", "as_block_sparsity", "as_prefill_mode", "as_hybrid_dense_blocks",
     "as_rsparse_prefill_workspace", "as_linear_prefill_rsparse", "as_linear_prefill_nm_split",
-    "as_select_stats", "as_checked_line",
+    "as_select_stats", "as_checked_line", "as_fp4_sf_bytes", "as_quant_fp4", "as_dequant_fp4",
+    "as_linear_prefill_fp4", "as_fp4_decode_bytes", "as_weight_prep_fp4", "as_linear_decode_fp4",
+    "as_norm_residual",
 ]
 AS_NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -62,6 +66,14 @@ class as_select_out(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in (
         "bitmask", "eta", "colnorm", "var_dense", "var_kept", "nu", "x_masked",
         "x_compact", "meta24", "x_masked_lo", "x_compact_lo", "bitmask24")]
+
+
+class as_norm_args(ctypes.Structure):
+    _fields_ = [*((name, ctypes.c_void_p) for name in ("r", "y", "r_out", "h", "post_w", "pre_w", "gate", "h_q",
+                                                       "h_sf", "h_scale")),
+                *((name, ctypes.c_int32) for name in ("r_dtype", "y_dtype", "h_dtype", "gate_rows", "post_norm",
+                                                      "fmt")),
+                *((name, ctypes.c_float) for name in ("res_scale", "eps", "w_offset"))]
 
 
 _P, _I, _F, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -102,6 +114,15 @@ _sig = {
     "as_linear_prefill_rsparse": ([ctypes.POINTER(as_select_out), _P, _P, _I, _I, _I, _P, _P,
                                    ctypes.POINTER(as_config), _I, _P, _P, _P, _P, _S, _P], _I),
     "as_hybrid_dense_blocks": ([_I, ctypes.c_double], _I),
+    "as_fp4_sf_bytes": ([_I, _I, _I], _S),
+    "as_quant_fp4": ([_P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
+    "as_dequant_fp4": ([_P, _P, _P, _I, _I, _I, _I, _P, _P], _I),
+    "as_linear_prefill_fp4": ([_P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P], _I),
+    "as_fp4_decode_bytes": ([_I, _I, _I], _S),
+    "as_weight_prep_fp4": ([_P, _P, _P, _I, _I, _I, _P, _P], _I),
+    "as_linear_decode_fp4": ([_P, _I, _I, _I, _I, _P, _I, _P, _P, ctypes.POINTER(as_config), _P, _P, _P, _P, _P, _S,
+                              _P], _I),
+    "as_norm_residual": ([ctypes.POINTER(as_norm_args), _I, _I, _P], _I),
 }
 for _name, (_args, _res) in _sig.items():
     _fn = getattr(_lib, _name)
@@ -389,6 +410,145 @@ def as_linear_prefill_nm_split(sel: as_select_out, T: int, W, cfg: as_config, y,
                                            _ptr(rowsum), _ptr(eta), _ptr(nu), _ptr(y), _ptr(dense_idx),
                                            _ptr(sparsity), _ptr(workspace), ws_bytes, _stream(stream)),
            "as_linear_prefill_nm_split")
+
+
+# ------------------------------------------- microscaled 4-bit, norm step
+def _on_current_device(*tensors) -> None:
+    """The library launches on the current device: refuse tensors of another."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _same(name: str, t, shape, dtype) -> None:
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _sf(name: str, t, rows: int, K: int, fmt: int) -> None:
+    n = as_fp4_sf_bytes(rows, K, fmt)
+    if t.dtype != torch.uint8 or t.numel() < n:
+        raise ValueError(f"{name} must hold at least {n} uint8 scale bytes")
+
+
+def as_fp4_sf_bytes(rows: int, K: int, fmt: int = AS_FP4_NV) -> int:
+    """Bytes of the scale buffer of rows x K microscaled values."""
+    n = _lib.as_fp4_sf_bytes(int(rows), int(K), int(fmt))
+    if n == 0:
+        raise ASError(AS_ERR_SHAPE, "as_fp4_sf_bytes")
+    return n
+
+
+def as_quant_fp4(x, codes, sf, row_scale=None, fmt: int = AS_FP4_NV, stream=None) -> None:
+    """x [rows, K] -> codes [rows, K/2] uint8, scale bytes, row_scale [rows]
+    (see include/actsparse.h for the formats)."""
+    _on_current_device(x, codes, sf, row_scale)
+    rows, K = x.shape
+    _same("codes", codes, (rows, K // 2), torch.uint8)
+    _sf("sf", sf, rows, K, fmt)
+    _same("row_scale", row_scale, (rows,), torch.float32)
+    _check(_lib.as_quant_fp4(_ptr(x), _dt(x), rows, K, fmt, _ptr(codes), _ptr(sf), _ptr(row_scale),
+                             _stream(stream)), "as_quant_fp4")
+
+
+def as_dequant_fp4(codes, sf, out, row_scale=None, fmt: int = AS_FP4_NV, stream=None) -> None:
+    """The values of codes and scales, written to out [rows, K]."""
+    _on_current_device(codes, sf, out, row_scale)
+    rows, K = out.shape
+    _same("codes", codes, (rows, K // 2), torch.uint8)
+    _sf("sf", sf, rows, K, fmt)
+    _same("row_scale", row_scale, (rows,), torch.float32)
+    _check(_lib.as_dequant_fp4(_ptr(codes), _ptr(sf), _ptr(row_scale), rows, K, fmt, _dt(out), _ptr(out),
+                               _stream(stream)), "as_dequant_fp4")
+
+
+def as_linear_prefill_fp4(xq, x_sf, Wq, w_sf, y, x_scale=None, w_scale=None, fmt: int = AS_FP4_NV,
+                          stream=None) -> None:
+    """y [T, n_out] = product of two quantised operands xq [T, K/2] and Wq [n_out, K/2]."""
+    _on_current_device(xq, x_sf, Wq, w_sf, y, x_scale, w_scale)
+    T, K = xq.shape[0], 2 * xq.shape[1]
+    n_out = Wq.shape[0]
+    _same("xq", xq, (T, K // 2), torch.uint8)
+    _same("Wq", Wq, (n_out, K // 2), torch.uint8)
+    _sf("x_sf", x_sf, T, K, fmt)
+    _sf("w_sf", w_sf, n_out, K, fmt)
+    _same("x_scale", x_scale, (T,), torch.float32)
+    _same("w_scale", w_scale, (n_out,), torch.float32)
+    _same("y", y, (T, n_out), y.dtype)
+    _check(_lib.as_linear_prefill_fp4(_ptr(xq), _ptr(x_sf), _ptr(x_scale), T, K, n_out, _ptr(Wq), _ptr(w_sf),
+                                      _ptr(w_scale), fmt, _dt(y), _ptr(y), _stream(stream)), "as_linear_prefill_fp4")
+
+
+def as_fp4_decode_bytes(n_out: int, K: int, fmt: int = AS_FP4_NV) -> int:
+    """Bytes of the decode layout of a quantised weight [n_out, K]."""
+    n = _lib.as_fp4_decode_bytes(int(n_out), int(K), int(fmt))
+    if n == 0:
+        raise ASError(AS_ERR_SHAPE, "as_fp4_decode_bytes")
+    return n
+
+
+def as_weight_prep_fp4(Wq, w_sf, Wd, w_scale=None, fmt: int = AS_FP4_NV, stream=None) -> None:
+    """The decode layout Wd of a quantised weight Wq [n_out, K/2]."""
+    _on_current_device(Wq, w_sf, Wd, w_scale)
+    n_out, K = Wq.shape[0], 2 * Wq.shape[1]
+    _same("Wq", Wq, (n_out, K // 2), torch.uint8)
+    _sf("w_sf", w_sf, n_out, K, fmt)
+    _same("w_scale", w_scale, (n_out,), torch.float32)
+    if Wd.dtype != torch.uint8 or Wd.numel() < as_fp4_decode_bytes(n_out, K, fmt):
+        raise ValueError("Wd is smaller than as_fp4_decode_bytes")
+    _check(_lib.as_weight_prep_fp4(_ptr(Wq), _ptr(w_sf), _ptr(w_scale), n_out, K, fmt, _ptr(Wd), _stream(stream)),
+           "as_weight_prep_fp4")
+
+
+def as_linear_decode_fp4(x, Wd, cfg: as_config, y, fmt: int = AS_FP4_NV, g=None, rowsum=None, mask_out=None,
+                         eta_out=None, colnorm_out=None, workspace=None, stream=None) -> None:
+    """as_linear_decode on the decode layout Wd of a 4-bit weight."""
+    _on_current_device(x, Wd, y, g, rowsum, mask_out, eta_out, colnorm_out, workspace)
+    T, K = x.shape
+    n_out = y.shape[1]
+    _same("y", y, (T, n_out), torch.bfloat16 if cfg.out_dtype == AS_BF16 else torch.float32)
+    if Wd.dtype != torch.uint8 or Wd.numel() < as_fp4_decode_bytes(n_out, K, fmt):
+        raise ValueError("Wd is smaller than as_fp4_decode_bytes")
+    _same("g", g, (K,), torch.float32)
+    _same("rowsum", rowsum, (n_out,), torch.float32)
+    _same("mask_out", mask_out, (T, (K + 31) // 32), torch.int32)
+    _same("eta_out", eta_out, (T,), torch.float32)
+    _same("colnorm_out", colnorm_out, (K,), torch.float32)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(_lib.as_linear_decode_fp4(_ptr(x), _dt(x), T, K, n_out, _ptr(Wd), fmt, _ptr(g), _ptr(rowsum),
+                                     ctypes.byref(cfg), _ptr(y), _ptr(mask_out), _ptr(eta_out), _ptr(colnorm_out),
+                                     _ptr(workspace), ws_bytes, _stream(stream)), "as_linear_decode_fp4")
+
+
+def as_norm_residual(r, y=None, r_out=None, h=None, post_w=None, pre_w=None, gate=None, res_scale: float = 1.0,
+                     eps: float = 1e-6, w_offset: float = 0.0, post_norm: bool = False, h_q=None, h_sf=None,
+                     h_scale=None, fmt: int = AS_FP4_NV, stream=None) -> None:
+    """r_out = res_scale r + gate norm(y) post_w;  h = norm(r_out) pre_w, as
+    values (h) and/or as a 4-bit operand (h_q, h_sf, h_scale).  Without y:
+    h = norm(r) pre_w."""
+    _on_current_device(r, y, r_out, h, post_w, pre_w, gate, h_q, h_sf, h_scale)
+    T, D = r.shape
+    _same("y", y, (T, D), y.dtype if y is not None else None)
+    _same("r_out", r_out, (T, D), r.dtype)
+    _same("h", h, (T, D), h.dtype if h is not None else None)
+    _same("post_w", post_w, (D,), torch.float32)
+    _same("pre_w", pre_w, (D,), torch.float32)
+    if gate is not None:
+        _same("gate", gate, (D,) if gate.dim() == 1 else (T, D), torch.float32)
+    if h_q is not None:
+        _same("h_q", h_q, (T, D // 2), torch.uint8)
+        if h_sf is not None:
+            _sf("h_sf", h_sf, T, D, fmt)
+        _same("h_scale", h_scale, (T,), torch.float32)
+    a = as_norm_args(r=_ptr(r), y=_ptr(y), r_out=_ptr(r_out), h=_ptr(h), post_w=_ptr(post_w), pre_w=_ptr(pre_w),
+                     gate=_ptr(gate), h_q=_ptr(h_q), h_sf=_ptr(h_sf), h_scale=_ptr(h_scale), r_dtype=_dt(r),
+                     y_dtype=_dt(y) if y is not None else AS_F32, h_dtype=_dt(h) if h is not None else AS_F32,
+                     gate_rows=T if gate is not None and gate.dim() == 2 else 1, post_norm=int(post_norm), fmt=fmt,
+                     res_scale=res_scale, eps=eps, w_offset=w_offset)
+    _check(_lib.as_norm_residual(ctypes.byref(a), T, D, _stream(stream)), "as_norm_residual")
 
 
 def as_stream_status(stream=None) -> int:

@@ -55,6 +55,14 @@ size_t decode_ws(int T, int K, int n_out, const as_config *cfg, int bf16)
     return bytes;
 }
 
+size_t decode_fp4_ws(int T, int K, const as_config *cfg)
+{
+    size_t bytes = round_up((size_t)T * ((K + 31) / 32) * sizeof(uint32_t), 256) +
+                   round_up((size_t)T * sizeof(float), 256);
+    if (cfg->score == AS_SCORE_CLACT) bytes += round_up(colnorm_workspace(T, K), 256);
+    return bytes;
+}
+
 size_t select_ws(int T, int K, const as_config *cfg)
 {
     return cfg->score == AS_SCORE_CLACT ? round_up(colnorm_workspace(T, K), 256) : 0;
@@ -103,6 +111,9 @@ size_t as_workspace_size(int op, int T, int K, int n_out, const as_config *cfg)
         if (T < 1 || T > AS_MAX_DECODE_T || n_out <= 0 || check_cfg(cfg, K) != AS_OK) return (size_t)-1;
         return decode_ws(T, K, n_out, cfg, 1) > decode_ws(T, K, n_out, cfg, 0) ? decode_ws(T, K, n_out, cfg, 1)
                                                                                 : decode_ws(T, K, n_out, cfg, 0);
+    case AS_OP_DECODE_FP4:
+        if (T < 1 || T > AS_MAX_DECODE_T || n_out <= 0 || check_cfg(cfg, K) != AS_OK) return (size_t)-1;
+        return decode_fp4_ws(T, K, cfg);
     case AS_OP_PREFILL:
         if (T <= 0 || n_out <= 0 || check_cfg(cfg, K) != AS_OK) return (size_t)-1;
         return 0;
@@ -355,6 +366,123 @@ as_status as_linear_prefill_fp8(const uint8_t *x8, const uint32_t *meta8, const 
     return e == cudaErrorNotSupported ? AS_ERR_UNSUPPORTED : cuda_status(e);
 }
 
+static bool fp4_fmt_ok(int fmt) { return fmt == AS_FP4_MX || fmt == AS_FP4_NV; }
+static bool fp4_k_ok(int K) { return K > 0 && K % 32 == 0 && K <= 131072; }
+
+size_t as_fp4_sf_bytes(int rows, int K, as_fp4 fmt)
+{
+    if (rows <= 0 || !fp4_k_ok(K) || !fp4_fmt_ok(fmt)) return 0;
+    return fp4_sf_bytes(rows, K, fmt);
+}
+
+as_status as_quant_fp4(const void *x, as_dtype dt, int rows, int K, as_fp4 fmt, uint8_t *codes, uint8_t *sf,
+                       float *row_scale, cudaStream_t stream)
+{
+    if (!x || !codes || !sf || rows <= 0 || !fp4_fmt_ok(fmt)) return AS_ERR_INVALID_ARG;
+    if (fmt == AS_FP4_NV && !row_scale) return AS_ERR_INVALID_ARG;
+    if (dt != AS_F32 && dt != AS_BF16) return AS_ERR_DTYPE;
+    if (!fp4_k_ok(K)) return AS_ERR_SHAPE;
+    for (const void *q : {x, (const void *)codes, (const void *)sf, (const void *)row_scale})
+        if (!aligned16(q)) return AS_ERR_ALIGN;
+    return cuda_status(launch_quant_fp4(x, dt == AS_BF16, rows, K, fmt, codes, sf, row_scale, stream));
+}
+
+as_status as_dequant_fp4(const uint8_t *codes, const uint8_t *sf, const float *row_scale, int rows, int K, as_fp4 fmt,
+                         as_dtype out_dtype, void *out, cudaStream_t stream)
+{
+    if (!codes || !sf || !out || rows <= 0 || !fp4_fmt_ok(fmt)) return AS_ERR_INVALID_ARG;
+    if (out_dtype != AS_F32 && out_dtype != AS_BF16) return AS_ERR_DTYPE;
+    if (!fp4_k_ok(K)) return AS_ERR_SHAPE;
+    for (const void *q : {(const void *)codes, (const void *)sf, (const void *)row_scale, (const void *)out})
+        if (!aligned16(q)) return AS_ERR_ALIGN;
+    return cuda_status(
+        launch_dequant_fp4(codes, sf, row_scale, rows, K, fmt, out_dtype == AS_BF16, out, stream));
+}
+
+as_status as_linear_prefill_fp4(const uint8_t *xq, const uint8_t *x_sf, const float *x_scale, int T, int K, int n_out,
+                                const uint8_t *Wq, const uint8_t *w_sf, const float *w_scale, as_fp4 fmt,
+                                as_dtype out_dtype, void *y, cudaStream_t stream)
+{
+    if (!xq || !x_sf || !Wq || !w_sf || !y || T <= 0 || n_out <= 0 || !fp4_fmt_ok(fmt)) return AS_ERR_INVALID_ARG;
+    if (out_dtype != AS_F32 && out_dtype != AS_BF16) return AS_ERR_DTYPE;
+    if (!fp4_k_ok(K) || n_out % 8 != 0) return AS_ERR_SHAPE;
+    for (const void *q : {(const void *)xq, (const void *)x_sf, (const void *)x_scale, (const void *)Wq,
+                          (const void *)w_sf, (const void *)w_scale, (const void *)y})
+        if (!aligned16(q)) return AS_ERR_ALIGN;
+    Fp4GemmArgs a{};
+    a.xq = xq;
+    a.x_sf = x_sf;
+    a.Wq = Wq;
+    a.w_sf = w_sf;
+    a.x_scale = x_scale;
+    a.w_scale = w_scale;
+    a.T = T;
+    a.K = K;
+    a.n_out = n_out;
+    a.fmt = fmt;
+    a.y = y;
+    a.out_bf16 = out_dtype == AS_BF16;
+    const cudaError_t e = launch_gemm_fp4(a, stream);
+    return e == cudaErrorNotSupported ? AS_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+size_t as_fp4_decode_bytes(int n_out, int K, as_fp4 fmt)
+{
+    if (n_out <= 0 || n_out % 8 != 0 || !fp4_k_ok(K) || !fp4_fmt_ok(fmt)) return 0;
+    return fp4_decode_bytes(n_out, K, fmt);
+}
+
+as_status as_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const float *w_scale, int n_out, int K,
+                             as_fp4 fmt, uint8_t *Wd, cudaStream_t stream)
+{
+    if (!Wq || !w_sf || !Wd || n_out <= 0 || !fp4_fmt_ok(fmt)) return AS_ERR_INVALID_ARG;
+    if (!fp4_k_ok(K) || n_out % 8 != 0) return AS_ERR_SHAPE;
+    for (const void *q : {(const void *)Wq, (const void *)w_sf, (const void *)w_scale, (const void *)Wd})
+        if (!aligned16(q)) return AS_ERR_ALIGN;
+    return cuda_status(launch_weight_prep_fp4(Wq, w_sf, w_scale, n_out, K, fmt, Wd, stream));
+}
+
+as_status as_norm_residual(const as_norm_args *a, int T, int D, cudaStream_t stream)
+{
+    if (!a || !a->r || T <= 0 || D <= 0) return AS_ERR_INVALID_ARG;
+    if (!a->r_out && !a->h && !a->h_q) return AS_ERR_INVALID_ARG;
+    if (!a->y && (a->r_out || a->gate || a->post_w || a->post_norm)) return AS_ERR_INVALID_ARG;
+    if ((a->h_q == nullptr) != (a->h_sf == nullptr) || (a->h_scale && !a->h_q)) return AS_ERR_INVALID_ARG;
+    if (a->post_norm != 0 && a->post_norm != 1) return AS_ERR_INVALID_ARG;
+    if (a->post_w && !a->post_norm) return AS_ERR_INVALID_ARG;
+    if (a->gate && a->gate_rows != 1 && a->gate_rows != T) return AS_ERR_INVALID_ARG;
+    if (!(a->eps >= 0.0f)) return AS_ERR_INVALID_ARG;  // also NaN
+    if (a->h_q && (!fp4_fmt_ok(a->fmt) || (a->fmt == AS_FP4_NV && !a->h_scale))) return AS_ERR_INVALID_ARG;
+    for (int d : {a->r_dtype, a->y ? a->y_dtype : a->r_dtype, a->h ? a->h_dtype : a->r_dtype})
+        if (d != AS_F32 && d != AS_BF16) return AS_ERR_DTYPE;
+    if (D % 8 != 0 || D > 32768 || (a->h_q && D % 32 != 0)) return AS_ERR_SHAPE;
+    for (const void *q : {a->r, a->y, (const void *)a->r_out, (const void *)a->h, (const void *)a->post_w,
+                          (const void *)a->pre_w, (const void *)a->gate, (const void *)a->h_q, (const void *)a->h_sf,
+                          (const void *)a->h_scale})
+        if (!aligned16(q)) return AS_ERR_ALIGN;
+    NormArgs n{};
+    n.r = a->r;
+    n.y = a->y;
+    n.r_out = a->r_out;
+    n.h = a->h;
+    n.post_w = a->post_w;
+    n.pre_w = a->pre_w;
+    n.gate = a->gate;
+    n.h_q = a->h_q;
+    n.h_sf = a->h_sf;
+    n.h_scale = a->h_scale;
+    n.r_bf16 = a->r_dtype == AS_BF16;
+    n.y_bf16 = a->y_dtype == AS_BF16;
+    n.h_bf16 = a->h_dtype == AS_BF16;
+    n.gate_rows = a->gate_rows;
+    n.post_norm = a->post_norm;
+    n.fmt = a->fmt;
+    n.res_scale = a->res_scale;
+    n.eps = a->eps;
+    n.w_offset = a->w_offset;
+    return cuda_status(launch_norm(n, T, D, stream));
+}
+
 as_status as_select(const void *x, as_dtype dt, int T, int K, const as_config *cfg, const float *chan_factor,
                     float *running_var, int var_first_batch, const as_select_out *out, void *workspace,
                     size_t ws_bytes, cudaStream_t stream)
@@ -541,6 +669,78 @@ as_status as_linear_decode(const void *x, as_dtype dt, int T, int K, int n_out, 
 }
 
 }  // extern "C"
+
+extern "C" as_status as_linear_decode_fp4(const void *x, as_dtype dt, int T, int K, int n_out, const uint8_t *Wd,
+                                          as_fp4 fmt, const float *g, const float *rowsum, const as_config *cfg,
+                                          void *y, uint32_t *mask_out, float *eta_out, float *colnorm_out,
+                                          void *workspace, size_t ws_bytes, cudaStream_t stream)
+{
+    as_status st = decode_check_args(x, dt, T, K, n_out, Wd, g, rowsum, cfg, y, mask_out, eta_out, colnorm_out);
+    if (st != AS_OK) return st;
+    if (!fp4_fmt_ok(fmt)) return AS_ERR_INVALID_ARG;
+    if (!fp4_k_ok(K)) return AS_ERR_SHAPE;
+    if (!aligned16(workspace)) return AS_ERR_ALIGN;
+    if (!workspace || ws_bytes < decode_fp4_ws(T, K, cfg)) return AS_ERR_WORKSPACE;
+    const int bf16 = dt == AS_BF16;
+    char *ws = static_cast<char *>(workspace);
+    uint32_t *mask = mask_out ? mask_out : reinterpret_cast<uint32_t *>(ws);
+    ws += round_up((size_t)T * ((K + 31) / 32) * sizeof(uint32_t), 256);
+    float *eta = eta_out ? eta_out : reinterpret_cast<float *>(ws);
+    ws += round_up((size_t)T * sizeof(float), 256);
+
+    DecodeFp4Args a{};
+    // keep-all without a shift or a mask to report needs no selection kernel
+    const bool select = cfg->sel != AS_SEL_ALL || cfg->dpts || mask_out;
+    const float *f = cfg->score == AS_SCORE_WEIGHT ? g : nullptr;
+    if (cfg->score == AS_SCORE_CLACT && (select || colnorm_out)) {
+        float *c = colnorm_out;
+        if (!c) c = reinterpret_cast<float *>(ws + colnorm_workspace(T, K) - (size_t)K * sizeof(float));
+        if (launch_colnorm(x, bf16, T, K, c, ws, stream) != cudaSuccess) return AS_ERR_CUDA;
+        f = c;
+    }
+    if (select) {
+        SelectArgs s{};
+        s.x = x;
+        s.bf16 = bf16;
+        s.T = T;
+        s.K = K;
+        s.score = cfg->score;
+        s.sel = cfg->sel;
+        s.n = cfg->n;
+        s.m = cfg->m;
+        s.k_keep = cfg->k_keep;
+        s.dpts = cfg->dpts;
+        s.tau = cfg->tau;
+        s.eta_static = cfg->dpts == AS_PTS_STATIC ? cfg->eta_static : nullptr;
+        s.f = f;
+        s.bitmask = mask;
+        s.eta = cfg->dpts ? eta : nullptr;
+        const cudaError_t se = (cfg->sel == AS_SEL_NM && bf16) ? launch_select_nm_decode(s, stream)
+                                                               : launch_select(s, stream, /*wide=*/1);
+        if (se != cudaSuccess) return AS_ERR_CUDA;
+        a.mask = mask;
+        a.after_select = 1;
+    }
+    a.x = x;
+    a.bf16 = bf16;
+    a.T = T;
+    a.K = K;
+    a.n_out = n_out;
+    a.Wd = Wd;
+    a.eta = cfg->dpts ? eta : nullptr;
+    a.rowsum = rowsum;
+    a.y = y;
+    a.out_bf16 = cfg->out_dtype == AS_BF16;
+    DecodeArgs d{};  // the expected share of channels that some token keeps
+    d.T = T;
+    d.K = K;
+    d.sel = cfg->sel;
+    d.n = cfg->n;
+    d.m = cfg->m;
+    d.k_keep = cfg->k_keep;
+    a.stream_all = !select || decode_streams_all(d);
+    return cuda_status(launch_decode_fp4(a, fmt, stream));
+}
 
 // Validation and GEMM arguments shared by the prefill entry points.
 static as_status prefill_args(const as_select_out *sel, const void *W, int T, int K, int n_out, const float *rowsum,

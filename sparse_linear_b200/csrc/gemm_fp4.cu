@@ -1,0 +1,594 @@
+// Product of two microscaled 4-bit operands on the block-scaled tensor cores:
+// tcgen05.mma kind::mxf4nvf4, K = 64 per instruction, E2M1 codes packed two
+// per byte in shared memory (128-byte swizzle, 256 channels per 128-byte row),
+// scales in tensor memory (scale_vec::4X: four E4M3 scales of 16 channels,
+// scale_vec::2X: two E8M0 scales of 32).
+//
+// Scales.  A 512-byte tile of the scale buffer (128 rows x 4 blocks) is what
+// tcgen05.cp.32x128b.warpx4 moves into four tensor-memory columns: row r of
+// the tile at lane r % 32 (repeated in each quarter of the lanes), column
+// r / 32, its four blocks in the column's bytes.  One tile covers one
+// instruction (NV) or two (MX: bytes 0-1, then 2-3, by the scale id of the
+// instruction descriptor).  256 rows of B take eight consecutive columns.
+//
+// k_gemm_fp4_pair   long prompts: 256 x 256 tiles on CTA pairs, as
+//                   k_gemm_dense_pair; each CTA holds its own 128 rows of A
+//                   with their scales, half of B, and all of B's scales.
+// k_gemm_fp4_few    few tokens: the weights are the M = 128 operand and the
+//                   tokens the N operand, so that every SM streams weights; K
+//                   is split over the CTAs of a cluster, whose sums are added
+//                   through distributed shared memory in rank order.
+// No load uses cluster multicast.  Every mbarrier wait is bounded.
+#include "common.cuh"
+#include "fp4.cuh"
+#include "kernels.cuh"
+
+namespace as {
+
+// D[tmem] (+)= (A * scales) (B * scales)^T; PAIR: over a CTA pair.
+template <int FMT, bool PAIR>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate)
+{
+    if constexpr (PAIR && FMT == AS_FP4_NV)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else if constexpr (FMT == AS_FP4_NV)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// 512 bytes (32 rows x 16 bytes) of shared memory -> 4 TMEM columns, repeated
+// in the four lane quarters; PAIR: in each CTA of the pair from its own.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_cp_sf(uint32_t taddr, uint64_t s_desc)
+{
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
+
+// Instruction descriptor of kind::mxf4nvf4: A and B format code 1 (E2M1) in
+// [7,10) and [10,13), N >> 3 in [17,23), scale format in bit 23 (0 E4M3, 1
+// E8M0), M >> 7 in [27,29); the scale ids of B in [4,6) and of A in [29,31)
+// are added per instruction.
+template <int FMT>
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N)
+{
+    return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (FMT == AS_FP4_MX ? 1u << 23 : 0u) |
+           ((uint32_t)(M >> 7) << 27);
+}
+
+template <int FMT>
+struct Fp4Cfg {
+    static constexpr int KB = 256;                         // channels per stage
+    static constexpr int SFT = FMT == AS_FP4_NV ? 4 : 2;   // scale tiles per stage and 128 rows
+    static constexpr int SFB = SFT * 512;                  // their bytes
+    // tile and scale id of instruction j (64 channels) of a stage
+    __device__ static constexpr int tile(int j) { return FMT == AS_FP4_NV ? j : j >> 1; }
+    __device__ static constexpr uint32_t ids(int j)
+    {
+        return FMT == AS_FP4_NV ? 0u : (((uint32_t)(j & 1) * 2u) << 4) | (((uint32_t)(j & 1) * 2u) << 29);
+    }
+};
+
+struct Fp4Params {
+    const float *x_scale, *w_scale;
+    void *y;
+    int T, K, n_out, out_bf16;
+    int m_tiles, n_tiles, k_blocks, kt;
+};
+
+// ------------------------------------------------------------- CTA pairs
+constexpr int FP_STAGES = 5;
+template <int FMT>
+struct FpPair {
+    static constexpr int A = 128 * 128, B = 128 * 128;
+    static constexpr int SA = Fp4Cfg<FMT>::SFB, SB = 2 * Fp4Cfg<FMT>::SFB;
+    static constexpr int STAGE = A + B + SA + SB;
+    static constexpr int SCOLS = 12 * Fp4Cfg<FMT>::SFT;  // TMEM columns of scales per stage
+    static constexpr size_t smem = 1024 + (size_t)FP_STAGES * STAGE + 256;
+    static_assert(PAIR_BN + FP_STAGES * SCOLS <= 512, "tensor memory");
+};
+
+// One output row's 32 columns from float32 accumulators: row scales, rounding
+// and stores (n_out % 8 == 0).
+__device__ __forceinline__ void fp4_store32(const Fp4Params &p, const uint32_t (&r)[32], int row, int col0, float xs)
+{
+    if (col0 >= p.n_out) return;
+    if (!as_in((long long)row * p.n_out + min(col0 + 31, p.n_out - 1), (long long)p.T * p.n_out)) return;
+#pragma unroll
+    for (int c8 = 0; c8 < 4; ++c8) {
+        const int col = col0 + 8 * c8;
+        if (col >= p.n_out) return;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * c8 + i]) * xs;
+        if (p.w_scale) {
+            const float4 a = *reinterpret_cast<const float4 *>(p.w_scale + col);
+            const float4 b = *reinterpret_cast<const float4 *>(p.w_scale + col + 4);
+            v[0] *= a.x; v[1] *= a.y; v[2] *= a.z; v[3] *= a.w;
+            v[4] *= b.x; v[5] *= b.y; v[6] *= b.z; v[7] *= b.w;
+        }
+        if (p.out_bf16) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.y) + (size_t)row * p.n_out + col) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.y) + (size_t)row * p.n_out + col);
+            o[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+}
+
+template <int FMT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
+    k_gemm_fp4_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, Fp4Params p)
+{
+    using C = Fp4Cfg<FMT>;
+    using P = FpPair<FMT>;
+    constexpr int S = FP_STAGES;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                            ~uintptr_t(1023));
+    unsigned char *sA = smem, *sB = sA + S * P::A, *sSA = sB + S * P::B, *sSB = sSA + S * P::SA;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sSB + S * P::SB);
+    uint64_t *full = bars, *empty = bars + S, *acc_full = bars + 2 * S, *acc_empty = bars + 2 * S + 1;
+    uint64_t *drain = bars + 2 * S + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 3);
+    int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int num_tiles = p.m_tiles * p.n_tiles;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);   // the leader's expect_tx arrival (+ both CTAs' bytes)
+            mbar_init(&empty[s], 1);  // one commit from the leader's MMA thread
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 16);  // 8 epilogue warps in each CTA (the leader's copy is used)
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmSA);
+        prefetch_tensormap(&tmSB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();  // barriers of both CTAs initialised before either uses the other's
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int tile = pair; tile < num_tiles && !*(volatile int *)abort_flag; tile += npairs) {
+                int mt, nt;
+                tile_coords(tile, p.m_tiles, p.n_tiles, mt, nt);
+                const int arow = mt * PAIR_BM + 128 * (int)rank;
+                const int brow = nt * PAIR_BN + 128 * (int)rank;
+                const int sa = (2 * mt + (int)rank) * p.kt, sb = 2 * nt * p.kt;  // scale tiles
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1)) { *(volatile int *)abort_flag = 1; break; }
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * P::STAGE);
+                    const uint32_t bar = mapa_u32(smem_u32(&full[stage]), 0);
+                    tma_load_2d_pair(sA + stage * P::A, &tmA, bar, kb * 128, arow);
+                    tma_load_2d_pair(sB + stage * P::B, &tmB, bar, kb * 128, brow);
+                    // the scales of the whole stage; tiles past K hold other
+                    // rows' scales and are not used
+                    tma_load_2d_pair(sSA + stage * P::SA, &tmSA, bar, 0, 2 * (sa + kb * C::SFT));
+                    tma_load_2d_pair(sSB + stage * P::SB, &tmSB, bar, 0, 2 * (sb + kb * C::SFT));
+                    tma_load_2d_pair(sSB + stage * P::SB + C::SFB, &tmSB, bar, 0, 2 * (sb + p.kt + kb * C::SFT));
+                    if (++stage == S) { stage = 0; phase ^= 1; }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (leader only)
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t idesc = idesc_fp4<FMT>(PAIR_BM, PAIR_BN);
+            int stage = 0;
+            uint32_t phase = 0;
+            int it = 0;
+            for (int tile = pair; tile < num_tiles && !*(volatile int *)abort_flag; tile += npairs, ++it) {
+                if (!mbar_wait(acc_empty, (it & 1) ^ 1)) { *(volatile int *)abort_flag = 1; break; }
+                tc_fence_after();
+                bool ok = true;
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (!mbar_wait(&full[stage], phase)) { ok = false; break; }
+                    tc_fence_after();
+                    const int steps = min(4, (p.K - kb * C::KB + 63) >> 6);
+                    const uint32_t sfa = tmem + PAIR_BN + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
+#pragma unroll
+                    for (int t = 0; t < C::SFT; ++t) {
+                        tmem_cp_sf<true>(sfa + 4 * t, sdesc_rows16(smem_u32(sSA + stage * P::SA + 512 * t)));
+                        tmem_cp_sf<true>(sfb + 8 * t, sdesc_rows16(smem_u32(sSB + stage * P::SB + 512 * t)));
+                        tmem_cp_sf<true>(sfb + 8 * t + 4,
+                                         sdesc_rows16(smem_u32(sSB + stage * P::SB + C::SFB + 512 * t)));
+                    }
+                    const uint64_t a_desc = sdesc_kmajor_sw128(smem_u32(sA + stage * P::A));
+                    const uint64_t b_desc = sdesc_kmajor_sw128(smem_u32(sB + stage * P::B));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < steps)
+                            mma_fp4<FMT, true>(tmem, a_desc + (uint64_t)((32 * j) >> 4),
+                                               b_desc + (uint64_t)((32 * j) >> 4), idesc | C::ids(j),
+                                               sfa + 4 * C::tile(j), sfb + 8 * C::tile(j), (kb | j) != 0);
+                    tc_commit_pair_mc(&empty[stage], 0x3);  // frees the stage in both CTAs
+                    if (++stage == S) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) { *(volatile int *)abort_flag = 1; break; }
+                tc_commit_pair_mc(acc_full, 0x3);
+            }
+            tc_commit_pair(drain);
+            mbar_wait(drain, 0);
+        }
+    } else {
+        // ------------------------------------------------ epilogue (warps 2..9)
+        const int q = warp & 3;           // TMEM lanes 32q..32q+31
+        const int h = (warp - 2) >> 2;    // accumulator columns [128h, 128h+128)
+        const uint32_t acc_empty_leader = mapa_u32(smem_u32(acc_empty), 0);
+        int it = 0;
+        for (int tile = pair; tile < num_tiles && !*(volatile int *)abort_flag; tile += npairs, ++it) {
+            int mt, nt;
+            tile_coords(tile, p.m_tiles, p.n_tiles, mt, nt);
+            if (!mbar_wait(acc_full, it & 1)) { *(volatile int *)abort_flag = 1; break; }
+            tc_fence_after();
+            uint32_t r[4][32];
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+                tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + 128 * h + 32 * ch, r[ch]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
+            const int row = mt * PAIR_BM + 128 * (int)rank + 32 * q + lane;
+            if (row >= p.T) continue;
+            const float xs = p.x_scale ? p.x_scale[row] : 1.0f;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) fp4_store32(p, r[ch], row, nt * PAIR_BN + 128 * h + 32 * ch, xs);
+        }
+    }
+
+    // Both CTAs' tensor memory stays allocated until the leader's last MMA
+    // has completed and both epilogues have read their accumulators.
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ------------------------------------------------------------ few tokens
+// Tile: 128 outputs (M) x N tokens.  Each CTA of a cluster takes a contiguous
+// part of the K blocks; one pass, so one accumulator and no accumulator ring.
+constexpr int FF_THREADS = 192;
+template <int FMT, int N>
+struct FpFew {
+    static constexpr int A = 128 * 128, B = N * 128;
+    static constexpr int NSB = (N + 127) / 128;  // scale row tiles of B
+    static constexpr int SA = Fp4Cfg<FMT>::SFB, SB = NSB * Fp4Cfg<FMT>::SFB;
+    static constexpr int STAGE = A + B + SA + SB;
+    static constexpr int SCOLS = 4 * (1 + NSB) * Fp4Cfg<FMT>::SFT;
+    static constexpr int STAGES = N <= 32 ? 8 : (N <= 64 ? 6 : 4);
+    static constexpr int RSTR = 128 + 4;                        // reduction row of a token, floats
+    static constexpr size_t ring = (size_t)STAGES * STAGE;
+    static constexpr size_t red = (size_t)N * RSTR * 4;
+    static constexpr size_t smem = 1024 + (ring > red ? ring : red) + 256;
+    static constexpr uint32_t TCOLS = N + STAGES * SCOLS <= 256 ? 256 : 512;
+    static_assert(N + STAGES * SCOLS <= 512, "tensor memory");
+};
+
+template <int FMT, int N>
+__global__ void __launch_bounds__(FF_THREADS, 1)
+    k_gemm_fp4_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, Fp4Params p)
+{
+    using C = Fp4Cfg<FMT>;
+    using P = FpFew<FMT, N>;
+    constexpr int S = P::STAGES;
+    extern __shared__ unsigned char smem_raw[];
+    // the reduction reads the peers' buffers at this CTA's offset: the
+    // dynamic window starts at the same address in every CTA of a kernel
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                            ~uintptr_t(1023));
+    unsigned char *sA = smem, *sB = sA + S * P::A, *sSA = sB + S * P::B, *sSB = sSA + S * P::SA;
+    float *red = reinterpret_cast<float *>(smem);  // after the main loop
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (P::ring > P::red ? P::ring : P::red));
+    uint64_t *full = bars, *empty = bars + S, *done = bars + 2 * S;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 1);
+    int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank(), nranks = gridDim.x;
+    const int ot = blockIdx.y, tt = blockIdx.z;  // output tile, token tile
+    const int per = (p.k_blocks + nranks - 1) / nranks;
+    const int kb0 = min(p.k_blocks, rank * per), kb1 = min(p.k_blocks, kb0 + per);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmSA);
+        prefetch_tensormap(&tmSB);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, P::TCOLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            const int sa = ot * p.kt, sb = tt * P::NSB * p.kt;  // tiles of fewer than 128 tokens: tt is 0
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&empty[stage], phase ^ 1)) { *(volatile int *)abort_flag = 1; break; }
+                mbar_arrive_expect_tx(&full[stage], P::STAGE);
+                tma_load_2d(sA + stage * P::A, &tmA, &full[stage], kb * 128, ot * 128);
+                tma_load_2d(sB + stage * P::B, &tmB, &full[stage], kb * 128, tt * N);
+                tma_load_2d(sSA + stage * P::SA, &tmSA, &full[stage], 0, 2 * (sa + kb * C::SFT));
+#pragma unroll
+                for (int c = 0; c < P::NSB; ++c)
+                    tma_load_2d(sSB + stage * P::SB + c * C::SFB, &tmSB, &full[stage], 0,
+                                2 * (sb + c * p.kt + kb * C::SFT));
+                if (++stage == S) { stage = 0; phase ^= 1; }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_fp4<FMT>(128, N);
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&full[stage], phase)) { *(volatile int *)abort_flag = 1; break; }
+                tc_fence_after();
+                const int steps = min(4, (p.K - kb * C::KB + 63) >> 6);
+                const uint32_t sfa = tmem + N + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
+#pragma unroll
+                for (int t = 0; t < C::SFT; ++t) {
+                    tmem_cp_sf<false>(sfa + 4 * t, sdesc_rows16(smem_u32(sSA + stage * P::SA + 512 * t)));
+#pragma unroll
+                    for (int c = 0; c < P::NSB; ++c)
+                        tmem_cp_sf<false>(sfb + 4 * P::NSB * t + 4 * c,
+                                          sdesc_rows16(smem_u32(sSB + stage * P::SB + c * C::SFB + 512 * t)));
+                }
+                const uint64_t a_desc = sdesc_kmajor_sw128(smem_u32(sA + stage * P::A));
+                const uint64_t b_desc = sdesc_kmajor_sw128(smem_u32(sB + stage * P::B));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < steps)
+                        mma_fp4<FMT, false>(tmem, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4),
+                                            idesc | C::ids(j), sfa + 4 * C::tile(j),
+                                            sfb + 4 * P::NSB * C::tile(j), (kb > kb0 || j > 0));
+                tc_commit(&empty[stage]);
+                if (++stage == S) { stage = 0; phase ^= 1; }
+            }
+            tc_commit(done);  // every MMA above has completed
+        }
+    }
+    // ---- all MMAs done: the accumulator (row = output, column = token) goes
+    // to shared memory transposed, over the drained ring
+    const bool some = kb1 > kb0;
+    bool ok = true;
+    if (warp >= 2) {
+        ok = mbar_wait(done, 0);
+        tc_fence_after();
+        const int q = warp & 3;
+        if (ok) {
+#pragma unroll
+            for (int c = 0; c < N / 16; ++c) {
+                uint32_t r[16];
+                if (some) {
+                    asm volatile(
+                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+                          "=r"(r[14]), "=r"(r[15])
+                        : "r"(tmem + ((uint32_t)(32 * q) << 16) + 16 * c));
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) red[(16 * c + i) * P::RSTR + 32 * q + lane] = __uint_as_float(r[i]);
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    cluster_sync_all();
+    tc_fence_after();
+    // ---- sum over the cluster in rank order; 8 consecutive outputs of a token per thread
+    const int tn = min(N, p.T - tt * N);
+    for (int i = rank * FF_THREADS + (int)threadIdx.x; i < tn * 16; i += nranks * FF_THREADS) {
+        const int t = i >> 4, c = (i & 15) * 8, row = tt * N + t, col = ot * 128 + c;
+        if (col >= p.n_out) continue;
+        const uint32_t at = smem_u32(red + t * P::RSTR + c);
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int r = 0; r < nranks; ++r) {
+            const uint32_t src = mapa_u32(at, (uint32_t)r);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float4 f;
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(src + 16 * k) : "memory");
+                v[4 * k] += f.x; v[4 * k + 1] += f.y; v[4 * k + 2] += f.z; v[4 * k + 3] += f.w;
+            }
+        }
+        if (!as_in((long long)row * p.n_out + col + 7, (long long)p.T * p.n_out)) continue;
+        const float xs = p.x_scale ? p.x_scale[row] : 1.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[k] *= xs;
+            if (p.w_scale) v[k] *= p.w_scale[col + k];
+        }
+        if (p.out_bf16) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                w[k] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.y) + (size_t)row * p.n_out + col) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.y) + (size_t)row * p.n_out + col);
+            o[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its sums
+    if (warp == 1) tmem_dealloc(tmem, P::TCOLS);
+}
+
+// ---------------------------------------------------------------- host side
+// Scale tiles as a 2-D uint32 tensor of 256-byte rows, box {64, 2 * tiles}.
+static bool make_map_sf(CUtensorMap *m, const void *base, uint64_t tiles, uint32_t box_tiles)
+{
+    PFN_encodeTiled_t enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {64, tiles * 2};
+    cuuint64_t strides[1] = {256};
+    cuuint32_t box[2] = {64, box_tiles * 2};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static Fp4Params fp4_params(const Fp4GemmArgs &a)
+{
+    Fp4Params p{};
+    p.x_scale = a.x_scale;
+    p.w_scale = a.w_scale;
+    p.y = a.y;
+    p.T = a.T;
+    p.K = a.K;
+    p.n_out = a.n_out;
+    p.out_bf16 = a.out_bf16;
+    p.k_blocks = (a.K + 255) / 256;
+    p.kt = fp4_sf_ktiles(a.K, a.fmt);
+    return p;
+}
+
+template <int FMT>
+static cudaError_t launch_fp4_pair(const Fp4GemmArgs &a, cudaStream_t st)
+{
+    CUtensorMap mA, mB, mSA, mSB;
+    Fp4Params p = fp4_params(a);
+    p.m_tiles = (a.T + PAIR_BM - 1) / PAIR_BM;
+    p.n_tiles = (a.n_out + PAIR_BN - 1) / PAIR_BN;
+    if (!make_map_u8(&mA, a.xq, (uint64_t)a.T, (uint64_t)a.K / 2, 128) ||
+        !make_map_u8(&mB, a.Wq, (uint64_t)a.n_out, (uint64_t)a.K / 2, 128) ||
+        !make_map_sf(&mSA, a.x_sf, (uint64_t)((a.T + 127) / 128) * p.kt, Fp4Cfg<FMT>::SFT) ||
+        !make_map_sf(&mSB, a.w_sf, (uint64_t)((a.n_out + 127) / 128) * p.kt, Fp4Cfg<FMT>::SFT))
+        return cudaErrorInvalidValue;
+    static int cached = -1;
+    const int clusters = pair_clusters_of(k_gemm_fp4_pair<FMT>, FpPair<FMT>::smem, cached);
+    if (clusters <= 0) return cudaErrorNotSupported;
+    static int done[64];
+    cudaError_t e = smem_limit_once(k_gemm_fp4_pair<FMT>, FpPair<FMT>::smem, done);
+    if (e != cudaSuccess) return e;
+    const int grid = 2 * std::min(p.m_tiles * p.n_tiles, clusters);
+    k_gemm_fp4_pair<FMT><<<grid, PAIR_THREADS, FpPair<FMT>::smem, st>>>(mA, mB, mSA, mSB, p);
+    return cudaGetLastError();
+}
+
+template <int FMT, int N>
+static cudaError_t launch_fp4_few(const Fp4GemmArgs &a, cudaStream_t st)
+{
+    using P = FpFew<FMT, N>;
+    CUtensorMap mA, mB, mSA, mSB;
+    Fp4Params p = fp4_params(a);
+    p.m_tiles = (a.n_out + 127) / 128;
+    p.n_tiles = (a.T + N - 1) / N;
+    if (!make_map_u8(&mA, a.Wq, (uint64_t)a.n_out, (uint64_t)a.K / 2, 128) ||
+        !make_map_u8(&mB, a.xq, (uint64_t)a.T, (uint64_t)a.K / 2, N) ||
+        !make_map_sf(&mSA, a.w_sf, (uint64_t)p.m_tiles * p.kt, Fp4Cfg<FMT>::SFT) ||
+        !make_map_sf(&mSB, a.x_sf, (uint64_t)((a.T + 127) / 128) * p.kt, Fp4Cfg<FMT>::SFT))
+        return cudaErrorInvalidValue;
+    static int done[64];
+    cudaError_t e = smem_limit_once(k_gemm_fp4_few<FMT, N>, P::smem, done);
+    if (e != cudaSuccess) return e;
+    int ranks = sm_count() / (p.m_tiles * p.n_tiles);
+    ranks = std::max(1, std::min({ranks, 8, p.k_blocks}));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks, p.m_tiles, p.n_tiles);
+    cfg.blockDim = dim3(FF_THREADS);
+    cfg.dynamicSmemBytes = P::smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_gemm_fp4_few<FMT, N>, mA, mB, mSA, mSB, p);
+}
+
+template <int FMT>
+static cudaError_t launch_fp4_t(const Fp4GemmArgs &a, cudaStream_t st)
+{
+    if (a.T <= 16) return launch_fp4_few<FMT, 16>(a, st);
+    if (a.T <= 32) return launch_fp4_few<FMT, 32>(a, st);
+    if (a.T <= 64) return launch_fp4_few<FMT, 64>(a, st);
+    if (a.T <= 256) return launch_fp4_few<FMT, 128>(a, st);
+    return launch_fp4_pair<FMT>(a, st);
+}
+
+cudaError_t launch_gemm_fp4(const Fp4GemmArgs &a, cudaStream_t st)
+{
+    return a.fmt == AS_FP4_NV ? launch_fp4_t<AS_FP4_NV>(a, st) : launch_fp4_t<AS_FP4_MX>(a, st);
+}
+
+}  // namespace as

@@ -79,6 +79,8 @@ bool decode_needs_select(int T, int K, int n_out, int bf16, int out_bf16, int se
 int decode_launch_count(const DecodeArgs &a, const DecodePlan &p);
 // True when a bf16 decode of this token pad and selection is one fused launch.
 bool decode_fused(int tpad, int sel, int K);
+// Whether nearly every channel is expected to be kept by some token.
+bool decode_streams_all(const DecodeArgs &a);
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &p, cudaStream_t st);
 
 // ------------------------------------------------------------ prefill GEMM
@@ -166,5 +168,51 @@ cudaError_t launch_sqrelu24_fp8(const void *z, int T, int K, uint8_t *x8, uint32
                                 uint32_t *bitmask, cudaStream_t st);
 cudaError_t launch_quant_rows_fp8(const void *W, int bf16, int n_out, int K, uint8_t *Wq, float *w_scale,
                                   cudaStream_t st);
+
+// Microscaled 4-bit (fp4.cu, gemm_fp4.cu, decode_fp4.cu).
+size_t fp4_sf_bytes(int rows, int K, int fmt);
+cudaError_t launch_quant_fp4(const void *x, int bf16, int rows, int K, int fmt, uint8_t *codes, uint8_t *sf,
+                             float *row_scale, cudaStream_t st);
+cudaError_t launch_dequant_fp4(const uint8_t *codes, const uint8_t *sf, const float *row_scale, int rows, int K,
+                               int fmt, int out_bf16, void *out, cudaStream_t st);
+struct Fp4GemmArgs {
+    const uint8_t *xq, *x_sf;  // [T, K/2] codes and their scale tiles
+    const uint8_t *Wq, *w_sf;  // [n_out, K/2]
+    const float *x_scale, *w_scale;  // row scales or nullptr
+    int T, K, n_out, fmt;
+    void *y;
+    int out_bf16;
+};
+cudaError_t launch_gemm_fp4(const Fp4GemmArgs &a, cudaStream_t st);
+size_t fp4_decode_bytes(int n_out, int K, int fmt);
+cudaError_t launch_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const float *w_scale, int n_out, int K,
+                                   int fmt, uint8_t *Wd, cudaStream_t st);
+struct DecodeFp4Args {
+    const void *x;
+    int bf16;
+    int T, K, n_out;
+    const uint8_t *Wd;
+    const float *rowf;     // set by the launcher: factors inside Wd
+    const uint32_t *mask;  // selection, or nullptr: every channel
+    const float *eta;      // token shift, or nullptr
+    const float *rowsum;
+    void *y;
+    int out_bf16;
+    int stream_all;        // read every channel's codes whatever the mask
+    int after_select;      // the previous kernel in the stream is this call's selection
+};
+cudaError_t launch_decode_fp4(DecodeFp4Args a, int fmt, cudaStream_t st);
+
+// Norm / residual step (norm.cu).
+struct NormArgs {
+    const void *r, *y;
+    void *r_out, *h;
+    const float *post_w, *pre_w, *gate;
+    uint8_t *h_q, *h_sf;
+    float *h_scale;
+    int r_bf16, y_bf16, h_bf16, gate_rows, post_norm, fmt;
+    float res_scale, eps, w_offset;
+};
+cudaError_t launch_norm(const NormArgs &a, int T, int D, cudaStream_t st);
 
 }  // namespace as

@@ -9,13 +9,14 @@ from __future__ import annotations
 
 import torch
 
-from . import (AS_BF16, AS_F32, AS_MODE_24, AS_MODE_DENSE, AS_MODE_SPLIT, AS_OP_AMBER, AS_OP_DECODE,
-               AS_OP_PREFILL, AS_OP_SELECT, AS_OP_WEIGHT_PREP, AS_SCORE_CLACT, AS_SCORE_MAG, AS_SEL_ALL, AS_SEL_NM,
-               as_block_sparsity, as_hybrid_dense_blocks, as_hybrid_workspace, as_linear_decode, as_linear_prefill,
+from . import (AS_BF16, AS_F32, AS_FP4_NV, AS_MODE_24, AS_MODE_DENSE, AS_MODE_SPLIT, AS_OP_AMBER, AS_OP_DECODE,
+               AS_OP_DECODE_FP4, AS_OP_PREFILL, AS_OP_SELECT, AS_OP_WEIGHT_PREP, AS_SCORE_CLACT, AS_SCORE_MAG, AS_SEL_ALL, AS_SEL_NM,
+               as_block_sparsity, as_dequant_fp4, as_fp4_decode_bytes, as_fp4_sf_bytes, as_hybrid_dense_blocks,
+               as_hybrid_workspace, as_linear_decode, as_linear_decode_fp4, as_linear_prefill, as_linear_prefill_fp4,
                as_linear_prefill_hybrid, as_linear_prefill_nm_split, as_linear_prefill_rsparse, as_meta24_words,
-               as_prefill_mode,
-               as_rsparse_prefill_workspace, as_select, as_weight_prep, as_weight_prep_amber, as_workspace_size,
-               config, select_out)
+               as_prefill_mode, as_quant_fp4,
+               as_rsparse_prefill_workspace, as_select, as_weight_prep, as_weight_prep_amber, as_weight_prep_fp4,
+               as_workspace_size, config, select_out)
 
 
 _MODE_NAMES = {AS_MODE_24: "2:4", AS_MODE_SPLIT: "split", AS_MODE_DENSE: "dense"}
@@ -227,4 +228,88 @@ class SparseLinear:
         return self.prefill_from(bufs, x.shape[0], stream=stream), bufs
 
 
-__all__ = ["SparseLinear", "workspace", "hybrid_mode", "dense_blocks_for", "AS_F32", "AS_BF16"]
+class Fp4Operand:
+    """Device buffers of [rows, K] microscaled 4-bit values: ``codes``, tiled
+    scale bytes ``sf`` and the float32 row scale ``scale``."""
+
+    def __init__(self, rows: int, K: int, fmt: int = AS_FP4_NV, device="cuda"):
+        self.rows, self.K, self.fmt = rows, K, fmt
+        self.codes = torch.empty(rows, K // 2, dtype=torch.uint8, device=device)
+        self.sf = torch.empty(as_fp4_sf_bytes(rows, K, fmt), dtype=torch.uint8, device=device)
+        self.scale = torch.empty(rows, dtype=torch.float32, device=device)
+
+    def quantise(self, x: torch.Tensor, stream=None) -> "Fp4Operand":
+        as_quant_fp4(x, self.codes, self.sf, self.scale, fmt=self.fmt, stream=stream)
+        return self
+
+    def values(self, dtype=torch.float32, stream=None) -> torch.Tensor:
+        out = torch.empty(self.rows, self.K, dtype=dtype, device=self.codes.device)
+        as_dequant_fp4(self.codes, self.sf, out, self.scale, fmt=self.fmt, stream=stream)
+        return out
+
+
+class Fp4Linear:
+    """y = prune(x) q(W)^T with W in microscaled 4 bits.
+
+    W: [n_out, K] bf16 or f32 CUDA tensor, quantised here.  ``cfg`` and
+    ``alpha`` as for ``SparseLinear``; g and rowsum are those of the
+    quantised weight.  ``keep_decode`` builds the decode layout.
+    """
+
+    def __init__(self, W: torch.Tensor, cfg, alpha: float = 0.0, fmt: int = AS_FP4_NV, keep_decode: bool = True):
+        self.n_out, self.K = W.shape
+        self.cfg, self.fmt = cfg, fmt
+        dev = W.device
+        self.weight = Fp4Operand(self.n_out, self.K, fmt, dev).quantise(W.contiguous())
+        self.g = torch.empty(self.K, dtype=torch.float32, device=dev)
+        self.rowsum = torch.empty(self.n_out, dtype=torch.float32, device=dev)
+        ws = workspace(as_workspace_size(AS_OP_WEIGHT_PREP, 0, self.K, self.n_out, None), dev)
+        as_weight_prep(self.weight.values(), float(alpha), g=self.g, rowsum=self.rowsum, workspace=ws)
+        self.Wd = None
+        if keep_decode:
+            self.Wd = torch.empty(as_fp4_decode_bytes(self.n_out, self.K, fmt), dtype=torch.uint8, device=dev)
+            as_weight_prep_fp4(self.weight.codes, self.weight.sf, self.Wd, w_scale=self.weight.scale, fmt=fmt)
+        self._ws = {}
+
+    def out_dtype(self) -> torch.dtype:
+        return torch.bfloat16 if self.cfg.out_dtype == AS_BF16 else torch.float32
+
+    def decode(self, x: torch.Tensor, y: torch.Tensor | None = None, mask_out=None, eta_out=None, colnorm_out=None,
+               stream=None) -> torch.Tensor:
+        """1 to 16 tokens; x is not quantised."""
+        T = x.shape[0]
+        if y is None:
+            y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
+        if T not in self._ws:
+            self._ws[T] = workspace(as_workspace_size(AS_OP_DECODE_FP4, T, self.K, self.n_out, self.cfg), x.device)
+        as_linear_decode_fp4(x, self.Wd, self.cfg, y, fmt=self.fmt, g=self.g, rowsum=self.rowsum, mask_out=mask_out,
+                             eta_out=eta_out, colnorm_out=colnorm_out, workspace=self._ws[T], stream=stream)
+        return y
+
+    def prefill_from(self, x: Fp4Operand, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The product with an operand that is already quantised."""
+        if x.fmt != self.fmt or x.K != self.K:
+            raise ValueError("the operand's format and K must be the weight's")
+        if y is None:
+            y = torch.empty(x.rows, self.n_out, dtype=self.out_dtype(), device=x.codes.device)
+        as_linear_prefill_fp4(x.codes, x.sf, self.weight.codes, self.weight.sf, y, x_scale=x.scale,
+                              w_scale=self.weight.scale, fmt=self.fmt, stream=stream)
+        return y
+
+    def prefill(self, x: torch.Tensor, stream=None) -> torch.Tensor:
+        """x pruned by cfg (no token shift, no VAR), quantised, multiplied."""
+        if self.cfg.dpts or self.cfg.var:
+            raise ValueError("4-bit prefill has no token shift and no VAR")
+        T = x.shape[0]
+        if self.cfg.sel != AS_SEL_ALL:
+            key = ("select", T)
+            if key not in self._ws:
+                self._ws[key] = workspace(as_workspace_size(AS_OP_SELECT, T, self.K, self.n_out, self.cfg), x.device)
+            kept = torch.empty_like(x)
+            as_select(x, self.cfg, select_out(x_masked=kept), chan_factor=self.g, workspace=self._ws[key],
+                      stream=stream)
+            x = kept
+        return self.prefill_from(Fp4Operand(T, self.K, self.fmt, x.device).quantise(x, stream), stream=stream)
+
+
+__all__ = ["SparseLinear", "Fp4Linear", "Fp4Operand", "workspace", "hybrid_mode", "dense_blocks_for", "AS_F32", "AS_BF16"]
