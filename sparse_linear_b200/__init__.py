@@ -12,6 +12,7 @@ library cannot be loaded raises immediately.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -413,27 +414,60 @@ def as_linear_prefill_nm_split(sel: as_select_out, T: int, W, cfg: as_config, y,
 
 
 # ------------------------------------------- microscaled 4-bit, norm step
-def _on_current_device(*tensors) -> None:
-    """The library launches on the current device: refuse tensors of another."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+# These calls are a few microseconds on the GPU, so their checks are too: one
+# pass over each tensor, sizes computed here rather than through the library.
+_U8, _F32, _BF16, _I32 = torch.uint8, torch.float32, torch.bfloat16, torch.int32
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
-def _same(name: str, t, shape, dtype) -> None:
+def _device(t) -> int:
+    """Device index of a call whose main tensor is `t`: the current device,
+    on which the library launches."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("libactsparse takes device tensors; got a CPU tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensor on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _arg(name: str, t, shape, dtype, dev: int):
+    """Address of a contiguous tensor of this shape, dtype and device; None stays None."""
     if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        return None
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("libactsparse takes contiguous (row-major) tensors")
+    return t.data_ptr()
 
 
-def _sf(name: str, t, rows: int, K: int, fmt: int) -> None:
-    n = as_fp4_sf_bytes(rows, K, fmt)
-    if t.dtype != torch.uint8 or t.numel() < n:
-        raise ValueError(f"{name} must hold at least {n} uint8 scale bytes")
+def _bytes(name: str, t, n: int, dev: int):
+    """Address of a uint8 buffer of at least n bytes."""
+    if t.dtype != _U8 or t.numel() < n:
+        raise ValueError(f"{name} must hold at least {n} uint8 bytes")
+    return _arg(name, t, t.shape, _U8, dev)
 
 
+def _call_stream(stream, dev: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _values_dtype(name: str, t) -> int:
+    if t.dtype != _BF16 and t.dtype != _F32:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return AS_BF16 if t.dtype == _BF16 else AS_F32
+
+
+def _workspace_bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+@functools.lru_cache(maxsize=None)
 def as_fp4_sf_bytes(rows: int, K: int, fmt: int = AS_FP4_NV) -> int:
     """Bytes of the scale buffer of rows x K microscaled values."""
     n = _lib.as_fp4_sf_bytes(int(rows), int(K), int(fmt))
@@ -442,46 +476,7 @@ def as_fp4_sf_bytes(rows: int, K: int, fmt: int = AS_FP4_NV) -> int:
     return n
 
 
-def as_quant_fp4(x, codes, sf, row_scale=None, fmt: int = AS_FP4_NV, stream=None) -> None:
-    """x [rows, K] -> codes [rows, K/2] uint8, scale bytes, row_scale [rows]
-    (see include/actsparse.h for the formats)."""
-    _on_current_device(x, codes, sf, row_scale)
-    rows, K = x.shape
-    _same("codes", codes, (rows, K // 2), torch.uint8)
-    _sf("sf", sf, rows, K, fmt)
-    _same("row_scale", row_scale, (rows,), torch.float32)
-    _check(_lib.as_quant_fp4(_ptr(x), _dt(x), rows, K, fmt, _ptr(codes), _ptr(sf), _ptr(row_scale),
-                             _stream(stream)), "as_quant_fp4")
-
-
-def as_dequant_fp4(codes, sf, out, row_scale=None, fmt: int = AS_FP4_NV, stream=None) -> None:
-    """The values of codes and scales, written to out [rows, K]."""
-    _on_current_device(codes, sf, out, row_scale)
-    rows, K = out.shape
-    _same("codes", codes, (rows, K // 2), torch.uint8)
-    _sf("sf", sf, rows, K, fmt)
-    _same("row_scale", row_scale, (rows,), torch.float32)
-    _check(_lib.as_dequant_fp4(_ptr(codes), _ptr(sf), _ptr(row_scale), rows, K, fmt, _dt(out), _ptr(out),
-                               _stream(stream)), "as_dequant_fp4")
-
-
-def as_linear_prefill_fp4(xq, x_sf, Wq, w_sf, y, x_scale=None, w_scale=None, fmt: int = AS_FP4_NV,
-                          stream=None) -> None:
-    """y [T, n_out] = product of two quantised operands xq [T, K/2] and Wq [n_out, K/2]."""
-    _on_current_device(xq, x_sf, Wq, w_sf, y, x_scale, w_scale)
-    T, K = xq.shape[0], 2 * xq.shape[1]
-    n_out = Wq.shape[0]
-    _same("xq", xq, (T, K // 2), torch.uint8)
-    _same("Wq", Wq, (n_out, K // 2), torch.uint8)
-    _sf("x_sf", x_sf, T, K, fmt)
-    _sf("w_sf", w_sf, n_out, K, fmt)
-    _same("x_scale", x_scale, (T,), torch.float32)
-    _same("w_scale", w_scale, (n_out,), torch.float32)
-    _same("y", y, (T, n_out), y.dtype)
-    _check(_lib.as_linear_prefill_fp4(_ptr(xq), _ptr(x_sf), _ptr(x_scale), T, K, n_out, _ptr(Wq), _ptr(w_sf),
-                                      _ptr(w_scale), fmt, _dt(y), _ptr(y), _stream(stream)), "as_linear_prefill_fp4")
-
-
+@functools.lru_cache(maxsize=None)
 def as_fp4_decode_bytes(n_out: int, K: int, fmt: int = AS_FP4_NV) -> int:
     """Bytes of the decode layout of a quantised weight [n_out, K]."""
     n = _lib.as_fp4_decode_bytes(int(n_out), int(K), int(fmt))
@@ -490,37 +485,74 @@ def as_fp4_decode_bytes(n_out: int, K: int, fmt: int = AS_FP4_NV) -> int:
     return n
 
 
+def as_quant_fp4(x, codes, sf, row_scale=None, fmt: int = AS_FP4_NV, stream=None) -> None:
+    """x [rows, K] -> codes [rows, K/2] uint8, scale bytes, row_scale [rows]
+    (see include/actsparse.h for the formats)."""
+    dev = _device(x)
+    rows, K = x.shape
+    code = _lib.as_quant_fp4(_arg("x", x, (rows, K), x.dtype, dev), _values_dtype("x", x), rows, K, fmt,
+                             _arg("codes", codes, (rows, K // 2), _U8, dev),
+                             _bytes("sf", sf, as_fp4_sf_bytes(rows, K, fmt), dev),
+                             _arg("row_scale", row_scale, (rows,), _F32, dev), _call_stream(stream, dev))
+    _check(code, "as_quant_fp4")
+
+
+def as_dequant_fp4(codes, sf, out, row_scale=None, fmt: int = AS_FP4_NV, stream=None) -> None:
+    """The values of codes and scales, written to out [rows, K]."""
+    dev = _device(out)
+    rows, K = out.shape
+    code = _lib.as_dequant_fp4(_arg("codes", codes, (rows, K // 2), _U8, dev),
+                               _bytes("sf", sf, as_fp4_sf_bytes(rows, K, fmt), dev),
+                               _arg("row_scale", row_scale, (rows,), _F32, dev), rows, K, fmt,
+                               _values_dtype("out", out), _arg("out", out, (rows, K), out.dtype, dev),
+                               _call_stream(stream, dev))
+    _check(code, "as_dequant_fp4")
+
+
+def as_linear_prefill_fp4(xq, x_sf, Wq, w_sf, y, x_scale=None, w_scale=None, fmt: int = AS_FP4_NV,
+                          stream=None) -> None:
+    """y [T, n_out] = product of two quantised operands xq [T, K/2] and Wq [n_out, K/2]."""
+    dev = _device(xq)
+    T, half = xq.shape
+    n_out, K = Wq.shape[0], 2 * half
+    code = _lib.as_linear_prefill_fp4(
+        _arg("xq", xq, (T, half), _U8, dev), _bytes("x_sf", x_sf, as_fp4_sf_bytes(T, K, fmt), dev),
+        _arg("x_scale", x_scale, (T,), _F32, dev), T, K, n_out, _arg("Wq", Wq, (n_out, half), _U8, dev),
+        _bytes("w_sf", w_sf, as_fp4_sf_bytes(n_out, K, fmt), dev), _arg("w_scale", w_scale, (n_out,), _F32, dev),
+        fmt, _values_dtype("y", y), _arg("y", y, (T, n_out), y.dtype, dev), _call_stream(stream, dev))
+    _check(code, "as_linear_prefill_fp4")
+
+
 def as_weight_prep_fp4(Wq, w_sf, Wd, w_scale=None, fmt: int = AS_FP4_NV, stream=None) -> None:
     """The decode layout Wd of a quantised weight Wq [n_out, K/2]."""
-    _on_current_device(Wq, w_sf, Wd, w_scale)
-    n_out, K = Wq.shape[0], 2 * Wq.shape[1]
-    _same("Wq", Wq, (n_out, K // 2), torch.uint8)
-    _sf("w_sf", w_sf, n_out, K, fmt)
-    _same("w_scale", w_scale, (n_out,), torch.float32)
-    if Wd.dtype != torch.uint8 or Wd.numel() < as_fp4_decode_bytes(n_out, K, fmt):
-        raise ValueError("Wd is smaller than as_fp4_decode_bytes")
-    _check(_lib.as_weight_prep_fp4(_ptr(Wq), _ptr(w_sf), _ptr(w_scale), n_out, K, fmt, _ptr(Wd), _stream(stream)),
-           "as_weight_prep_fp4")
+    dev = _device(Wq)
+    n_out, half = Wq.shape
+    K = 2 * half
+    code = _lib.as_weight_prep_fp4(_arg("Wq", Wq, (n_out, half), _U8, dev),
+                                   _bytes("w_sf", w_sf, as_fp4_sf_bytes(n_out, K, fmt), dev),
+                                   _arg("w_scale", w_scale, (n_out,), _F32, dev), n_out, K, fmt,
+                                   _bytes("Wd", Wd, as_fp4_decode_bytes(n_out, K, fmt), dev),
+                                   _call_stream(stream, dev))
+    _check(code, "as_weight_prep_fp4")
 
 
 def as_linear_decode_fp4(x, Wd, cfg: as_config, y, fmt: int = AS_FP4_NV, g=None, rowsum=None, mask_out=None,
                          eta_out=None, colnorm_out=None, workspace=None, stream=None) -> None:
     """as_linear_decode on the decode layout Wd of a 4-bit weight."""
-    _on_current_device(x, Wd, y, g, rowsum, mask_out, eta_out, colnorm_out, workspace)
+    dev = _device(x)
     T, K = x.shape
     n_out = y.shape[1]
-    _same("y", y, (T, n_out), torch.bfloat16 if cfg.out_dtype == AS_BF16 else torch.float32)
-    if Wd.dtype != torch.uint8 or Wd.numel() < as_fp4_decode_bytes(n_out, K, fmt):
-        raise ValueError("Wd is smaller than as_fp4_decode_bytes")
-    _same("g", g, (K,), torch.float32)
-    _same("rowsum", rowsum, (n_out,), torch.float32)
-    _same("mask_out", mask_out, (T, (K + 31) // 32), torch.int32)
-    _same("eta_out", eta_out, (T,), torch.float32)
-    _same("colnorm_out", colnorm_out, (K,), torch.float32)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(_lib.as_linear_decode_fp4(_ptr(x), _dt(x), T, K, n_out, _ptr(Wd), fmt, _ptr(g), _ptr(rowsum),
-                                     ctypes.byref(cfg), _ptr(y), _ptr(mask_out), _ptr(eta_out), _ptr(colnorm_out),
-                                     _ptr(workspace), ws_bytes, _stream(stream)), "as_linear_decode_fp4")
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+    code = _lib.as_linear_decode_fp4(
+        _arg("x", x, (T, K), x.dtype, dev), _values_dtype("x", x), T, K, n_out,
+        _bytes("Wd", Wd, as_fp4_decode_bytes(n_out, K, fmt), dev), fmt, _arg("g", g, (K,), _F32, dev),
+        _arg("rowsum", rowsum, (n_out,), _F32, dev), ctypes.byref(cfg),
+        _arg("y", y, (T, n_out), _BF16 if cfg.out_dtype == AS_BF16 else _F32, dev),
+        _arg("mask_out", mask_out, (T, (K + 31) // 32), _I32, dev), _arg("eta_out", eta_out, (T,), _F32, dev),
+        _arg("colnorm_out", colnorm_out, (K,), _F32, dev),
+        None if workspace is None else workspace.data_ptr(), _workspace_bytes(workspace), _call_stream(stream, dev))
+    _check(code, "as_linear_decode_fp4")
 
 
 def as_norm_residual(r, y=None, r_out=None, h=None, post_w=None, pre_w=None, gate=None, res_scale: float = 1.0,
@@ -529,26 +561,21 @@ def as_norm_residual(r, y=None, r_out=None, h=None, post_w=None, pre_w=None, gat
     """r_out = res_scale r + gate norm(y) post_w;  h = norm(r_out) pre_w, as
     values (h) and/or as a 4-bit operand (h_q, h_sf, h_scale).  Without y:
     h = norm(r) pre_w."""
-    _on_current_device(r, y, r_out, h, post_w, pre_w, gate, h_q, h_sf, h_scale)
-    T, D = r.shape
-    _same("y", y, (T, D), y.dtype if y is not None else None)
-    _same("r_out", r_out, (T, D), r.dtype)
-    _same("h", h, (T, D), h.dtype if h is not None else None)
-    _same("post_w", post_w, (D,), torch.float32)
-    _same("pre_w", pre_w, (D,), torch.float32)
-    if gate is not None:
-        _same("gate", gate, (D,) if gate.dim() == 1 else (T, D), torch.float32)
-    if h_q is not None:
-        _same("h_q", h_q, (T, D // 2), torch.uint8)
-        if h_sf is not None:
-            _sf("h_sf", h_sf, T, D, fmt)
-        _same("h_scale", h_scale, (T,), torch.float32)
-    a = as_norm_args(r=_ptr(r), y=_ptr(y), r_out=_ptr(r_out), h=_ptr(h), post_w=_ptr(post_w), pre_w=_ptr(pre_w),
-                     gate=_ptr(gate), h_q=_ptr(h_q), h_sf=_ptr(h_sf), h_scale=_ptr(h_scale), r_dtype=_dt(r),
-                     y_dtype=_dt(y) if y is not None else AS_F32, h_dtype=_dt(h) if h is not None else AS_F32,
-                     gate_rows=T if gate is not None and gate.dim() == 2 else 1, post_norm=int(post_norm), fmt=fmt,
-                     res_scale=res_scale, eps=eps, w_offset=w_offset)
-    _check(_lib.as_norm_residual(ctypes.byref(a), T, D, _stream(stream)), "as_norm_residual")
+    dev = _device(r)
+    T, D = full = r.shape
+    per_token = gate is not None and gate.dim() == 2
+    a = as_norm_args(
+        _arg("r", r, full, r.dtype, dev), _arg("y", y, full, y.dtype, dev) if y is not None else None,
+        _arg("r_out", r_out, full, r.dtype, dev), _arg("h", h, full, h.dtype, dev) if h is not None else None,
+        _arg("post_w", post_w, (D,), _F32, dev), _arg("pre_w", pre_w, (D,), _F32, dev),
+        _arg("gate", gate, full if per_token else (D,), _F32, dev),
+        _arg("h_q", h_q, (T, D // 2), _U8, dev),
+        _bytes("h_sf", h_sf, as_fp4_sf_bytes(T, D, fmt), dev) if h_sf is not None else None,
+        _arg("h_scale", h_scale, (T,), _F32, dev),
+        _values_dtype("r", r), _values_dtype("y", y) if y is not None else AS_F32,
+        _values_dtype("h", h) if h is not None else AS_F32, T if per_token else 1, int(post_norm), fmt, res_scale,
+        eps, w_offset)
+    _check(_lib.as_norm_residual(ctypes.byref(a), T, D, _call_stream(stream, dev)), "as_norm_residual")
 
 
 def as_stream_status(stream=None) -> int:

@@ -899,12 +899,12 @@ static cudaError_t launch_gemm_t(const GemmArgs &a, cudaStream_t st)
 // Number of 2-CTA clusters of k_gemm_sp_pair that fit on the device at once
 // (0 if the query fails).
 template <typename KernelT>
-static int pair_clusters_of(KernelT kernel, size_t smem, int &cached)
+static int pair_clusters_of(KernelT kernel, size_t smem, int &cached, int threads = PAIR_THREADS)
 {
     if (cached >= 0) return cached;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2 * 74, 1, 1);
-    cfg.blockDim = dim3(PAIR_THREADS, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -14,6 +14,11 @@
 // k_gemm_fp4_pair   long prompts: 256 x 256 tiles on CTA pairs, as
 //                   k_gemm_dense_pair; each CTA holds its own 128 rows of A
 //                   with their scales, half of B, and all of B's scales.
+//                   Its scales go to tensor memory through the registers of
+//                   four warps (tcgen05.st), not by tcgen05.cp: a stage needs
+//                   12 copies of about 45 clocks beside 512 clocks of MMAs,
+//                   and the two overlap only in part (717 clocks together);
+//                   the stores leave the MMAs at 513.
 // k_gemm_fp4_few    few tokens: the weights are the M = 128 operand and the
 //                   tokens the N operand, so that every SM streams weights; K
 //                   is split over the CTAs of a cluster, whose sums are added
@@ -99,55 +104,47 @@ struct Fp4Params {
 };
 
 // ------------------------------------------------------------- CTA pairs
+//   warp 0       TMA producer of A and B (both CTAs' bytes count on the
+//                leader's barrier).
+//   warp 1       tensor-memory allocation; lane 0 of the leader issues MMAs.
+//   warps 2-9    epilogue: (lane quarter, column half) per warp.
+//   warps 10-13  scales: shared memory -> registers -> tensor memory, then an
+//                arrival on the leader's full barrier (both CTAs' warps).
+//   warp 14      TMA producer of the scales.
+// The scales have a shared-memory ring of their own (FP_SF slots), so that
+// they are at hand when a stage (and its slot in tensor memory) is freed.
 constexpr int FP_STAGES = 5;
+constexpr int FP_SF = 8;
+constexpr int FP_THREADS = 480;
 template <int FMT>
 struct FpPair {
     static constexpr int A = 128 * 128, B = 128 * 128;
     static constexpr int SA = Fp4Cfg<FMT>::SFB, SB = 2 * Fp4Cfg<FMT>::SFB;
-    static constexpr int STAGE = A + B + SA + SB;
-    static constexpr int SCOLS = 12 * Fp4Cfg<FMT>::SFT;  // TMEM columns of scales per stage
-    static constexpr size_t smem = 1024 + (size_t)FP_STAGES * STAGE + 256;
+    static constexpr int SCOLS = 12 * Fp4Cfg<FMT>::SFT;  // TMEM columns of scales per K block
+    static constexpr size_t smem = 1024 + (size_t)FP_STAGES * (A + B) + (size_t)FP_SF * (SA + SB) + 256;
     static_assert(PAIR_BN + FP_STAGES * SCOLS <= 512, "tensor memory");
 };
 
-// One output row's 32 columns from float32 accumulators: row scales, rounding
-// and stores (n_out % 8 == 0).
-__device__ __forceinline__ void fp4_store32(const Fp4Params &p, const uint32_t (&r)[32], int row, int col0, float xs)
+// 32 lanes x N columns from N registers.
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t *r)
 {
-    if (col0 >= p.n_out) return;
-    if (!as_in((long long)row * p.n_out + min(col0 + 31, p.n_out - 1), (long long)p.T * p.n_out)) return;
-#pragma unroll
-    for (int c8 = 0; c8 < 4; ++c8) {
-        const int col = col0 + 8 * c8;
-        if (col >= p.n_out) return;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * c8 + i]) * xs;
-        if (p.w_scale) {
-            const float4 a = *reinterpret_cast<const float4 *>(p.w_scale + col);
-            const float4 b = *reinterpret_cast<const float4 *>(p.w_scale + col + 4);
-            v[0] *= a.x; v[1] *= a.y; v[2] *= a.z; v[3] *= a.w;
-            v[4] *= b.x; v[5] *= b.y; v[6] *= b.z; v[7] *= b.w;
-        }
-        if (p.out_bf16) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t *>(&h);
-            }
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.y) + (size_t)row * p.n_out + col) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.y) + (size_t)row * p.n_out + col);
-            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
+    if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    else {
+        static_assert(N == 16, "8 or 16 columns");
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::
+                "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+            : "memory");
     }
 }
 
 template <int FMT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
     k_gemm_fp4_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, Fp4Params p)
 {
@@ -157,12 +154,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                             ~uintptr_t(1023));
-    unsigned char *sA = smem, *sB = sA + S * P::A, *sSA = sB + S * P::B, *sSB = sSA + S * P::SA;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sSB + S * P::SB);
-    uint64_t *full = bars, *empty = bars + S, *acc_full = bars + 2 * S, *acc_empty = bars + 2 * S + 1;
-    uint64_t *drain = bars + 2 * S + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 3);
+    unsigned char *sA = smem, *sB = sA + S * P::A, *sSA = sB + S * P::B, *sSB = sSA + FP_SF * P::SA;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sSB + FP_SF * P::SB);
+    uint64_t *full = bars, *empty = full + S;                // A and B
+    uint64_t *sf_land = empty + S, *sf_read = sf_land + FP_SF;    // scales in shared memory
+    uint64_t *acc_full = sf_read + FP_SF, *acc_empty = acc_full + 1, *drain = acc_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+    __shared__ __align__(16) float s_ws[8][128];  // every epilogue warp's weight row scales
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -171,8 +170,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);   // the leader's expect_tx arrival (+ both CTAs' bytes)
-            mbar_init(&empty[s], 1);  // one commit from the leader's MMA thread
+            mbar_init(&full[s], 9);     // the leader's expect_tx arrival (+ both CTAs' bytes), 8 scale warps
+            mbar_init(&empty[s], 1);    // one commit from the leader's MMA thread
+        }
+        for (int s = 0; s < FP_SF; ++s) {
+            mbar_init(&sf_land[s], 1);  // own expect_tx arrival (+ own scale bytes)
+            mbar_init(&sf_read[s], 4);  // own scale warps
         }
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 16);  // 8 epilogue warps in each CTA (the leader's copy is used)
@@ -203,18 +206,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                 tile_coords(tile, p.m_tiles, p.n_tiles, mt, nt);
                 const int arow = mt * PAIR_BM + 128 * (int)rank;
                 const int brow = nt * PAIR_BN + 128 * (int)rank;
-                const int sa = (2 * mt + (int)rank) * p.kt, sb = 2 * nt * p.kt;  // scale tiles
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1)) { *(volatile int *)abort_flag = 1; break; }
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * P::STAGE);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (P::A + P::B));
                     const uint32_t bar = mapa_u32(smem_u32(&full[stage]), 0);
                     tma_load_2d_pair(sA + stage * P::A, &tmA, bar, kb * 128, arow);
                     tma_load_2d_pair(sB + stage * P::B, &tmB, bar, kb * 128, brow);
-                    // the scales of the whole stage; tiles past K hold other
-                    // rows' scales and are not used
-                    tma_load_2d_pair(sSA + stage * P::SA, &tmSA, bar, 0, 2 * (sa + kb * C::SFT));
-                    tma_load_2d_pair(sSB + stage * P::SB, &tmSB, bar, 0, 2 * (sb + kb * C::SFT));
-                    tma_load_2d_pair(sSB + stage * P::SB + C::SFB, &tmSB, bar, 0, 2 * (sb + p.kt + kb * C::SFT));
                     if (++stage == S) { stage = 0; phase ^= 1; }
                 }
             }
@@ -226,22 +223,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
             int stage = 0;
             uint32_t phase = 0;
             int it = 0;
+            // A barrier's answer takes some 240 clocks here even when it is
+            // ready: the next stage is asked for before this one's MMAs issue.
+            bool ready = false;
             for (int tile = pair; tile < num_tiles && !*(volatile int *)abort_flag; tile += npairs, ++it) {
                 if (!mbar_wait(acc_empty, (it & 1) ^ 1)) { *(volatile int *)abort_flag = 1; break; }
-                tc_fence_after();
                 bool ok = true;
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!mbar_wait(&full[stage], phase)) { ok = false; break; }
+                    if (!ready && !mbar_wait(&full[stage], phase)) { ok = false; break; }
                     tc_fence_after();
+                    const int next = stage + 1 == S ? 0 : stage + 1;
+                    const uint32_t nphase = stage + 1 == S ? phase ^ 1 : phase;
+                    ready = mbar_try_wait(&full[next], nphase);
                     const int steps = min(4, (p.K - kb * C::KB + 63) >> 6);
                     const uint32_t sfa = tmem + PAIR_BN + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
-#pragma unroll
-                    for (int t = 0; t < C::SFT; ++t) {
-                        tmem_cp_sf<true>(sfa + 4 * t, sdesc_rows16(smem_u32(sSA + stage * P::SA + 512 * t)));
-                        tmem_cp_sf<true>(sfb + 8 * t, sdesc_rows16(smem_u32(sSB + stage * P::SB + 512 * t)));
-                        tmem_cp_sf<true>(sfb + 8 * t + 4,
-                                         sdesc_rows16(smem_u32(sSB + stage * P::SB + C::SFB + 512 * t)));
-                    }
                     const uint64_t a_desc = sdesc_kmajor_sw128(smem_u32(sA + stage * P::A));
                     const uint64_t b_desc = sdesc_kmajor_sw128(smem_u32(sB + stage * P::B));
 #pragma unroll
@@ -250,14 +245,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                             mma_fp4<FMT, true>(tmem, a_desc + (uint64_t)((32 * j) >> 4),
                                                b_desc + (uint64_t)((32 * j) >> 4), idesc | C::ids(j),
                                                sfa + 4 * C::tile(j), sfb + 8 * C::tile(j), (kb | j) != 0);
-                    tc_commit_pair_mc(&empty[stage], 0x3);  // frees the stage in both CTAs
-                    if (++stage == S) { stage = 0; phase ^= 1; }
+                    tc_commit_pair_mc(&empty[stage], 0x3);  // frees the stage and its scales in both CTAs
+                    stage = next;
+                    phase = nphase;
                 }
                 if (!ok) { *(volatile int *)abort_flag = 1; break; }
                 tc_commit_pair_mc(acc_full, 0x3);
             }
             tc_commit_pair(drain);
             mbar_wait(drain, 0);
+        }
+    } else if (warp == 14) {
+        // ------------------------------------------------ TMA producer of scales
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int tile = pair; tile < num_tiles && !*(volatile int *)abort_flag; tile += npairs) {
+                int mt, nt;
+                tile_coords(tile, p.m_tiles, p.n_tiles, mt, nt);
+                const int sa = (2 * mt + (int)rank) * p.kt, sb = 2 * nt * p.kt;  // scale tiles
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (!mbar_wait(&sf_read[stage], phase ^ 1)) { *(volatile int *)abort_flag = 1; break; }
+                    // the scales of the whole K block; tiles past K hold other
+                    // rows' scales and are not used
+                    mbar_arrive_expect_tx(&sf_land[stage], P::SA + P::SB);
+                    tma_load_2d(sSA + stage * P::SA, &tmSA, &sf_land[stage], 0, 2 * (sa + kb * C::SFT));
+                    tma_load_2d(sSB + stage * P::SB, &tmSB, &sf_land[stage], 0, 2 * (sb + kb * C::SFT));
+                    tma_load_2d(sSB + stage * P::SB + C::SFB, &tmSB, &sf_land[stage], 0,
+                                2 * (sb + p.kt + kb * C::SFT));
+                    if (++stage == FP_SF) { stage = 0; phase ^= 1; }
+                }
+            }
+        }
+    } else if (warp >= 10) {
+        // ------------------------------------------------ scales (warps 10..13)
+        const int q = warp & 3;
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, sphase = 0;
+        const uint32_t full0 = mapa_u32(smem_u32(full), 0);
+        for (int tile = pair; tile < num_tiles && !*(volatile int *)abort_flag; tile += npairs) {
+            for (int kb = 0; kb < p.k_blocks; ++kb) {
+                if (!mbar_wait(&sf_land[stage], phase)) { *(volatile int *)abort_flag = 1; break; }
+                // a tile's 16 bytes of lane l are its columns 0..3; B's two
+                // row tiles of one K tile lie side by side in tensor memory
+                const unsigned char *a = sSA + stage * P::SA + 16 * lane, *b = sSB + stage * P::SB + 16 * lane;
+                uint32_t ra[4 * C::SFT], rb[8 * C::SFT];
+#pragma unroll
+                for (int t = 0; t < C::SFT; ++t) {
+                    *reinterpret_cast<uint4 *>(ra + 4 * t) = *reinterpret_cast<const uint4 *>(a + 512 * t);
+                    *reinterpret_cast<uint4 *>(rb + 8 * t) = *reinterpret_cast<const uint4 *>(b + 512 * t);
+                    *reinterpret_cast<uint4 *>(rb + 8 * t + 4) =
+                        *reinterpret_cast<const uint4 *>(b + C::SFB + 512 * t);
+                }
+                if (!mbar_wait(&empty[slot], sphase ^ 1)) { *(volatile int *)abort_flag = 1; break; }
+                tc_fence_after();
+                const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + PAIR_BN + slot * P::SCOLS;
+                tmem_st<4 * C::SFT>(col, ra);
+                tmem_st<4 * C::SFT>(col + 4 * C::SFT, rb);
+                tmem_st<4 * C::SFT>(col + 8 * C::SFT, rb + 4 * C::SFT);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();  // all lanes have read the slot and written theirs
+                if (lane == 0) {
+                    mbar_arrive(&sf_read[stage]);
+                    mbar_arrive_cluster(full0 + 8u * (uint32_t)slot);
+                }
+                if (++stage == FP_SF) { stage = 0; phase ^= 1; }
+                if (++slot == S) { slot = 0; sphase ^= 1; }
+            }
         }
     } else {
         // ------------------------------------------------ epilogue (warps 2..9)
@@ -268,21 +323,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
         for (int tile = pair; tile < num_tiles && !*(volatile int *)abort_flag; tile += npairs, ++it) {
             int mt, nt;
             tile_coords(tile, p.m_tiles, p.n_tiles, mt, nt);
+            // the tile's weight row scales, while its MMAs run
+            const int col0 = nt * PAIR_BN + 128 * h;
+            float *ws = s_ws[warp - 2];
+            __syncwarp();  // the last tile's reads
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ws[32 * i + lane] = p.w_scale && col0 + 32 * i + lane < p.n_out ? p.w_scale[col0 + 32 * i + lane] : 1.0f;
+            __syncwarp();
+            const int row = mt * PAIR_BM + 128 * (int)rank + 32 * q + lane;
+            const bool row_ok = row < p.T;
+            const float xs = p.x_scale && row_ok ? p.x_scale[row] : 1.0f;
             if (!mbar_wait(acc_full, it & 1)) { *(volatile int *)abort_flag = 1; break; }
             tc_fence_after();
-            uint32_t r[4][32];
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + 128 * h;
+            if (p.out_bf16) {  // rounded in registers, so that the accumulator is free before the stores
+                uint32_t out[4][16];
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-                tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + 128 * h + 32 * ch, r[ch]);
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
-            const int row = mt * PAIR_BM + 128 * (int)rank + 32 * q + lane;
-            if (row >= p.T) continue;
-            const float xs = p.x_scale ? p.x_scale[row] : 1.0f;
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(taddr + 32 * ch, r);
+                    tmem_ld_wait();
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) fp4_store32(p, r[ch], row, nt * PAIR_BN + 128 * h + 32 * ch, xs);
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 w = *reinterpret_cast<const float2 *>(ws + 32 * ch + 2 * i);
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * i]) * xs * w.x,
+                                                                       __uint_as_float(r[2 * i + 1]) * xs * w.y);
+                        out[ch][i] = *reinterpret_cast<const uint32_t *>(&v);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
+                if (row_ok) {
+                    __nv_bfloat16 *yr = static_cast<__nv_bfloat16 *>(p.y) + (size_t)row * p.n_out;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (col0 + 8 * c < p.n_out &&
+                            as_in((long long)row * p.n_out + col0 + 8 * c + 7, (long long)p.T * p.n_out))
+                            *reinterpret_cast<uint4 *>(yr + col0 + 8 * c) = *reinterpret_cast<uint4 *>(&out[c >> 2][4 * (c & 3)]);
+                }
+            } else {
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(taddr + 32 * ch, r);
+                    tmem_ld_wait();
+                    if (row_ok) {
+                        float *yr = static_cast<float *>(p.y) + (size_t)row * p.n_out;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const int col = col0 + 32 * ch + 4 * c;
+                            if (col < p.n_out && as_in((long long)row * p.n_out + col + 3, (long long)p.T * p.n_out)) {
+                                const float4 w = *reinterpret_cast<const float4 *>(ws + 32 * ch + 4 * c);
+                                *reinterpret_cast<float4 *>(yr + col) =
+                                    make_float4(__uint_as_float(r[4 * c]) * xs * w.x,
+                                                __uint_as_float(r[4 * c + 1]) * xs * w.y,
+                                                __uint_as_float(r[4 * c + 2]) * xs * w.z,
+                                                __uint_as_float(r[4 * c + 3]) * xs * w.w);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
+            }
         }
     }
 
@@ -533,13 +639,13 @@ static cudaError_t launch_fp4_pair(const Fp4GemmArgs &a, cudaStream_t st)
         !make_map_sf(&mSB, a.w_sf, (uint64_t)((a.n_out + 127) / 128) * p.kt, Fp4Cfg<FMT>::SFT))
         return cudaErrorInvalidValue;
     static int cached = -1;
-    const int clusters = pair_clusters_of(k_gemm_fp4_pair<FMT>, FpPair<FMT>::smem, cached);
+    const int clusters = pair_clusters_of(k_gemm_fp4_pair<FMT>, FpPair<FMT>::smem, cached, FP_THREADS);
     if (clusters <= 0) return cudaErrorNotSupported;
     static int done[64];
     cudaError_t e = smem_limit_once(k_gemm_fp4_pair<FMT>, FpPair<FMT>::smem, done);
     if (e != cudaSuccess) return e;
     const int grid = 2 * std::min(p.m_tiles * p.n_tiles, clusters);
-    k_gemm_fp4_pair<FMT><<<grid, PAIR_THREADS, FpPair<FMT>::smem, st>>>(mA, mB, mSA, mSB, p);
+    k_gemm_fp4_pair<FMT><<<grid, FP_THREADS, FpPair<FMT>::smem, st>>>(mA, mB, mSA, mSB, p);
     return cudaGetLastError();
 }
 
