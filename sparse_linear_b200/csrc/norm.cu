@@ -99,7 +99,7 @@ __device__ __forceinline__ void norm_store_fp4(const NormArgs &a, const float (&
 }
 
 template <int NT, int CH>
-__global__ void __launch_bounds__(NT) k_norm_residual(NormArgs a, int T, int D, int kt)
+__global__ void __launch_bounds__(NT, NT * CH <= 1024 ? 1024 / NT : 1) k_norm_residual(NormArgs a, int T, int D, int kt)
 {
     __shared__ float red[2][NT / 32];
     __shared__ uint32_t s_max[NT / 32];
@@ -122,8 +122,9 @@ __global__ void __launch_bounds__(NT) k_norm_residual(NormArgs a, int T, int D, 
         }
     }
     if (a.y) {
-        float y[CH][8];
+        float y[CH][8], g[CH][8];
         float ss = 0.0f;
+        const float *gate = a.gate ? a.gate + (a.gate_rows == 1 ? 0 : row) : nullptr;
 #pragma unroll
         for (int r = 0; r < CH; ++r) {
             const int c = r * NT + tid;
@@ -132,6 +133,7 @@ __global__ void __launch_bounds__(NT) k_norm_residual(NormArgs a, int T, int D, 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[r][e] = 0.0f;
             }
+            if (gate && c < nch) load8f(gate + 8 * (size_t)c, g[r]);  // before the reduction waits
         }
         float rms = 1.0f;
         if (a.post_norm) {
@@ -141,19 +143,17 @@ __global__ void __launch_bounds__(NT) k_norm_residual(NormArgs a, int T, int D, 
                 for (int e = 0; e < 8; ++e) ss = fmaf(y[r][e], y[r][e], ss);
             rms = __frsqrt_rn(block_sum<NT>(ss, red[0]) / (float)D + a.eps);
         }
-        const float *gate = a.gate ? a.gate + (a.gate_rows == 1 ? 0 : row) : nullptr;
 #pragma unroll
         for (int r = 0; r < CH; ++r) {
             const int c = r * NT + tid;
             if (c >= nch) continue;
-            float w[8], g[8];
+            float w[8];
             if (a.post_w) load8f(a.post_w + 8 * (size_t)c, w);
-            if (gate) load8f(gate + 8 * (size_t)c, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float u = y[r][e] * rms;
                 if (a.post_w) u *= a.w_offset + w[e];
-                if (gate) u *= g[e];
+                if (gate) u *= g[r][e];
                 v[r][e] = fmaf(a.res_scale, v[r][e], u);
             }
             if (a.r_out && as_in((long long)row + 8 * c + 7, (long long)T * D))
@@ -200,9 +200,9 @@ cudaError_t launch_norm(const NormArgs &a, int T, int D, cudaStream_t st)
 {
     const int nch = D / 8;
     if (nch <= 128) return launch_norm_t<128, 1>(a, T, D, st);
-    if (nch <= 256) return launch_norm_t<128, 2>(a, T, D, st);
+    if (nch <= 256) return launch_norm_t<256, 1>(a, T, D, st);
     if (nch <= 512) return launch_norm_t<256, 2>(a, T, D, st);
-    if (nch <= 1024) return launch_norm_t<256, 4>(a, T, D, st);
+    if (nch <= 1024) return launch_norm_t<512, 2>(a, T, D, st);
     if (nch <= 2048) return launch_norm_t<512, 4>(a, T, D, st);
     return launch_norm_t<1024, 4>(a, T, D, st);
 }
