@@ -577,8 +577,8 @@ as_status as_linear_prefill_fp4(const uint8_t *xq, const uint8_t *x_sf, const fl
 /* Decode weights, once per layer: the quantised weight [n_out, K] re-laid so
  * that a kept channel's codes are contiguous for 128 output columns.  Wd is
  * opaque, as_fp4_decode_bytes(n_out, K, fmt) bytes, and carries w_scale
- * (NULL: 1).  An output whose row holds a NaN scale gives NaN.  AS_FP4_MX
- * weights below 2^-126 times the row's largest block scale may lose bits.
+ * (NULL: 1).  An output whose row holds a NaN scale gives NaN; AS_FP4_MX
+ * blocks whose scale is below 2^-126 times their row's largest count as zero.
  * as_fp4_decode_bytes is host-only and 0 if the arguments are invalid. */
 size_t as_fp4_decode_bytes(int n_out, int K, as_fp4 fmt);
 as_status as_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const float *w_scale, int n_out, int K,
@@ -588,8 +588,9 @@ as_status as_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const float
  *   y = prune(x) W^T (+ eta_t rowsum_o with a token shift),
  * W the values that Wq stands for.  Scores, selection, shift and the outputs
  * mask_out, eta_out, colnorm_out are those of as_linear_decode; x is not
- * quantised (the kept values enter the tensor cores as one to three bf16
- * parts: exactly for float32 output, to 2^-17 for bf16 output).  g and rowsum
+ * quantised: each token is scaled by a power of two and its kept values enter
+ * the tensor cores with 22 bits (all 8 of an unshifted bf16 value), values
+ * below 2^-28 of the token's largest with an error of 2^-39 of it.  g and rowsum
  * describe the same W (as_weight_prep on its values).  Only the codes of
  * channels that some token keeps are read.
  *   x [T, K] in `dt`; K % 32 == 0, n_out % 8 == 0; cfg->var is not supported.

@@ -4,21 +4,22 @@
 // Weight layout (k_fp4_decode_layout, once per layer).  Slices of 128 output
 // columns; in a slice one unit per scale block of B channels: B rows of 64
 // bytes (the block's channels), then the 128 outputs' scales.  Inside 16
-// channels, row 4r + q holds channel 4q + r; its 8-byte piece g holds outputs
-// o(p, g) = 16 (p >> 1) + 8 (p & 1) + g, p = 0..15: exactly what lane
-// (g, q) of an m16n8k16 fragment needs, so a lane's four pieces need no
-// exchange with other lanes.
-//   A 16-bit half of a piece holds four codes with their bits placed so that
-// a shift and a mask give bf16 patterns: magnitude bits at 6..8 (the two
-// lowest exponent bits and the top mantissa bit), sign at 15.  Such a pattern
-// is the E2M1 value times 2^-126 (E2M1 subnormals are bf16 subnormals).
-//   Scales are recoded to 8 bits that shift into a bf16 of scale * 2^119
-// (NV: 5 exponent and 3 mantissa bits, which hold E4M3's subnormals as
-// normal numbers; MX: the exponent, relative to the row's largest so that
-// the range always fits).  pattern * scale is then the weight times 2^-7
-// (MX: times a power of two of its row), exact in bf16: at most 2 + 4
-// significant bits.  A float32 factor per output undoes the power of two and
-// carries the weight's row scale.
+// channels, row 4r + q holds channel 4q + r; its 8-byte piece g holds the codes
+// of outputs o(p, g) = 16 (p >> 1) + 8 (p & 1) + g, p = 0..15, four bits each:
+// exactly what lane (g, q) of an m16n8k16 fragment needs, so a lane's four
+// pieces need no exchange with other lanes.  Two rows' words interleave (two
+// shifts and two selects per 16 codes) into bytes that hold the codes of a
+// channel pair for one output, and one conversion per byte (cvt f16x2.e2m1x2)
+// gives the A fragment register: codes enter the tensor cores as they are.
+//   Scales multiply the products of their 16 channels in float32:
+//   acc += s * (codes x), one fused step per block and output, which also keeps
+//   every sum of the tensor core short.  MX scales are stored relative to the
+//   row's largest; a float32 factor per output carries that power of two and
+//   the weight's row scale.
+//   Kept values enter as one or two f16 parts after scaling each token by a
+//   power of two that puts its largest |x| in the CTA's range of K at 2^14: bf16
+//   values are exact from 2^-28 of the largest up, smaller ones err by at most
+//   2^-39 of it; two parts hold 22 bits of a float32 value.
 #include "common.cuh"
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -64,16 +65,9 @@ __global__ void __launch_bounds__(256) k_fp4_rowf(const uint8_t *__restrict__ w_
     bad = __reduce_max_sync(0xffffffffu, bad);
     if (lane == 0) {
         const float ws = o < n_out ? (w_scale ? w_scale[o] : 1.0f) : 0.0f;
-        rowf[o] = bad ? __uint_as_float(0x7FFFFFFFu) : ldexpf(ws, fmt == AS_FP4_MX ? (int)m - 128 : 7);
+        rowf[o] = bad ? __uint_as_float(0x7FFFFFFFu) : (fmt == AS_FP4_MX ? ldexpf(ws, (int)m - 127) : ws);
         top[o] = (int)m;
     }
-}
-
-// Code j of a half: magnitude and sign bits at their places (see above).
-__device__ __forceinline__ uint32_t df_place(uint32_t code, int j)
-{
-    const int mp[4] = {6, 9, 0, 3}, sp[4] = {15, 14, 13, 12};
-    return ((code & 7u) << mp[j]) | ((code >> 3) << sp[j]);
 }
 
 // CTA = (scale block, slice), 128 threads = outputs.
@@ -95,24 +89,9 @@ __global__ void __launch_bounds__(DF_COLS) k_fp4_decode_layout(const uint8_t *__
 #pragma unroll
         for (int i = 0; i < B / 8; ++i) w[i] = src[i];
         const uint32_t s = w_sf[fp4_sf_byte(o, blk, fp4_sf_ktiles(K, FMT))];
-        if constexpr (FMT == AS_FP4_MX) {
-            const int f = s == 255u ? 0 : (int)s - top[o] + 254;  // a NaN scale shows in the output's factor
-            scale = f > 0 ? (uint32_t)f : 0u;
-        } else {
-            const uint32_t e = (s >> 3) & 15u, m = s & 7u;
-            if ((s & 127u) != 127u && (s & 127u) != 0u) {
-                if (e > 0) {
-                    scale = ((e + 15u) << 3) | m;  // exponent e - 7, field + 22
-                } else {                            // m * 2^-9, normalised
-                    const uint32_t h = 31u - (uint32_t)__clz((int)m);
-                    scale = ((h + 13u) << 3) | ((m << (3u - h)) & 7u);
-                }
-            }
-        }
-        if (scale == 0u) {  // a zero scale stands for zeros
-#pragma unroll
-            for (int i = 0; i < B / 8; ++i) w[i] = 0u;
-        }
+        // a NaN scale shows in the output's factor
+        if constexpr (FMT == AS_FP4_MX) scale = s == 255u ? 0u : (uint32_t)max((int)s - top[o] + 127, 0);
+        else scale = (s & 127u) == 127u ? 0u : s & 127u;
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) nib[i][c] = (uint8_t)((w[i >> 3] >> (4 * (i & 7))) & 15u);
@@ -123,12 +102,10 @@ __global__ void __launch_bounds__(DF_COLS) k_fp4_decode_layout(const uint8_t *__
         const int r = (row & 15) >> 2, q = row & 3, ch = (row & ~15) + 4 * q + r;
         uint32_t word = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int p = wd * 8 + h * 4 + j;
-                word |= df_place(nib[ch][16 * (p >> 1) + 8 * (p & 1) + g], j) << (16 * h);
-            }
+        for (int k = 0; k < 8; ++k) {
+            const int p = wd * 8 + k;
+            word |= (uint32_t)nib[ch][16 * (p >> 1) + 8 * (p & 1) + g] << (4 * k);
+        }
         reinterpret_cast<uint32_t *>(unit)[i] = word;
     }
     const int p = 2 * (c >> 4) + ((c >> 3) & 1), g = c & 7;
@@ -155,14 +132,14 @@ cudaError_t launch_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const
 // part of K; its warps take 16-channel steps in turn.  A lane copies its own
 // pieces of the kept rows (cp.async, a ring of its own in shared memory),
 // turns them into A fragments and multiplies with the kept values of x, which
-// the CTA stages in shared memory as PARTS bf16 arrays (zero where a token
+// the CTA stages in shared memory as PARTS f16 arrays (zero where a token
 // dropped the channel, so rows that were not loaded do not matter).  The
 // warps' sums are added in shared memory and the cluster's through
 // distributed shared memory, both in a fixed order.
 template <int NT, int PARTS>
 struct DfCfg {
     static constexpr int TP = 8 * NT;
-    static constexpr int KSUB = NT * PARTS == 1 ? 2048 : 1024;  // channels of x staged at a time
+    static constexpr int KSUB = NT * PARTS <= 2 ? 2048 : 1024;  // channels of x staged at a time
     static constexpr int XS = KSUB + 16;                        // row stride: token rows 8 banks apart
     static constexpr size_t xbytes = (size_t)PARTS * TP * XS * 2;
     static constexpr size_t ring = (size_t)DF_WARPS * DF_DEPTH * DF_STAGE;
@@ -171,13 +148,6 @@ struct DfCfg {
     static constexpr size_t smem = big + xbytes;
     static constexpr int per_sm = smem <= 110 * 1024 ? 2 : 1;
 };
-
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
 {
@@ -191,6 +161,46 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// Four bytes of two codes each -> four f16x2.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&r)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, const float (&c)[4])
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// The scales of outputs p (bytes of sc) as float32.
+template <int FMT>
+__device__ __forceinline__ void df_scales(uint32_t sc, float (&f)[4])
+{
+    if constexpr (FMT == AS_FP4_MX) {
+        f[0] = __uint_as_float((sc & 0xFFu) << 23);
+        f[1] = __uint_as_float((sc & 0xFF00u) << 15);
+        f[2] = __uint_as_float((sc & 0xFF0000u) << 7);
+        f[3] = __uint_as_float((sc >> 24) << 23);
+    } else {
+        const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(sc & 0xFFFFu), __NV_E4M3);
+        const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(sc >> 16), __NV_E4M3);
+        const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
+        f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+    }
+}
+
 template <int NT, int PARTS, int FMT>
 __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode_fp4(DecodeFp4Args a)
 {
@@ -198,10 +208,11 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
     constexpr int TP = C::TP;
     extern __shared__ __align__(16) unsigned char smem[];
     float *red = reinterpret_cast<float *>(smem);  // after the main loop
-    __nv_bfloat16 *xs = reinterpret_cast<__nv_bfloat16 *>(smem + C::big);
+    __half *xs = reinterpret_cast<__half *>(smem + C::big);
     __shared__ uint32_t s_keep[TP][C::KSUB / 32];
     __shared__ uint32_t s_union[C::KSUB / 32];
-    __shared__ float s_eta[TP];
+    __shared__ float s_eta[TP], s_mul[TP], s_inv[TP];  // shift; power of two into and out of f16's range
+    __shared__ uint32_t s_max[TP];
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, q4 = lane & 3;
@@ -212,6 +223,76 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
     const uint8_t *wslice = a.Wd + (size_t)slice * (size_t)(K / fp4_block(FMT)) * df_unit(FMT);
     const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (DF_DEPTH * DF_STAGE);
 
+    // step s of this warp in the part that starts at word ws covers channels
+    // 32 ws + 16 (DF_WARPS s + warp); it has `mine` of them
+    auto steps_of = [&](int ws) {
+        const int n = 2 * min(C::KSUB / 32, w1 - ws);
+        return n > warp ? (n - warp + DF_WARPS - 1) / DF_WARPS : 0;
+    };
+    auto issue = [&](int ws, int s, int mine, bool all) {
+        if (s < mine) {
+            const int lb = DF_WARPS * s + warp, b = 2 * ws + lb;
+            const uint32_t keep = all ? 0xFFFFu : (s_union[lb >> 1] >> (16 * (lb & 1))) & 0xFFFFu;
+            const uint8_t *unit = FMT == AS_FP4_NV ? wslice + (size_t)b * df_unit(FMT)
+                                                   : wslice + (size_t)(b >> 1) * df_unit(FMT) + (b & 1) * 1024;
+            const uint32_t dst = ring + (uint32_t)(s % DF_DEPTH) * DF_STAGE;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if ((keep >> (4 * q4 + r)) & 1u) cp_async8(dst + r * 256 + lane * 8, unit + r * 256 + q4 * 64 + g8 * 8);
+            const uint8_t *sc = FMT == AS_FP4_NV ? unit + 1024 : wslice + (size_t)(b >> 1) * df_unit(FMT) + 2048;
+            if (lane < 8) cp_async16(dst + 1024 + lane * 16, sc + lane * 16, 16u);
+        }
+        cp_async_commit();
+    };
+    auto prologue = [&](int ws, bool all) {
+        const int mine = steps_of(ws);
+#pragma unroll
+        for (int s = 0; s < DF_DEPTH - 1; ++s) issue(ws, s, mine, all);
+    };
+    auto load_x = [&](int t, int c, float (&v)[8]) {  // channels c .. c+7 of token t
+        const size_t at = (size_t)t * K + (size_t)c;
+        if (a.bf16) load8(static_cast<const __nv_bfloat16 *>(a.x) + at, v);
+        else load8(static_cast<const float *>(a.x) + at, v);
+    };
+
+    // The select kernel lets this one start after its own wait, so everything
+    // before that kernel in the stream (x and the weights) is complete.  What
+    // does not depend on the selection comes before the wait for it: the
+    // tokens' largest |x| and, if every channel is wanted, the first weights.
+    if (!a.after_select) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.stream_all) prologue(w0, true);
+    if (tid < TP) s_max[tid] = 0u;
+    __syncthreads();
+    {
+        const int tiles = (w1 - w0 + 7) >> 3;  // 256 channels
+        for (int i = warp; i < T * tiles; i += DF_WARPS) {
+            const int t = i / tiles, c = 32 * w0 + 256 * (i % tiles) + 8 * lane;
+            uint32_t m = 0;
+            if (c < 32 * w1 && as_in((long long)t * K + c + 7, (long long)T * K)) {
+                float v[8];
+                load_x(t, c, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t b = __float_as_uint(v[e]) & 0x7FFFFFFFu;
+                    m = max(m, b < F32_INF_BITS ? b : 0u);
+                }
+            }
+            m = __reduce_max_sync(0xffffffffu, m);
+            if (lane == 0) atomicMax(&s_max[t], m);
+        }
+    }
+    __syncthreads();
+    if (a.after_select) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid < TP) {
+        const float eta = (a.eta && tid < T) ? a.eta[tid] : 0.0f;
+        s_eta[tid] = eta;
+        const uint32_t top = __float_as_uint(__uint_as_float(s_max[tid]) + fabsf(eta));  // bounds |x - eta|
+        int e = top == 0u ? 0 : 14 - ((int)(top >> 23) - 127);
+        e = e > 126 ? 126 : (e < -113 ? -113 : e);
+        s_mul[tid] = pow2f(e);
+        s_inv[tid] = pow2f(-e);
+    }
+
     float acc[8][NT][4];
 #pragma unroll
     for (int m = 0; m < 8; ++m)
@@ -220,43 +301,9 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
 
-    bool waited = false;
     for (int ws = w0; ws < w1; ws += C::KSUB / 32) {
-        const int nw = min(C::KSUB / 32, w1 - ws), nsteps = 2 * nw;  // 16-channel steps of this part
-        // step s of this warp covers channels 32 ws + 16 (DF_WARPS s + warp)
-        const int mine = nsteps > warp ? (nsteps - warp + DF_WARPS - 1) / DF_WARPS : 0;
-        auto issue = [&](int s, bool all) {
-            if (s < mine) {
-                const int lb = DF_WARPS * s + warp, b = 2 * ws + lb;
-                const uint32_t keep = all ? 0xFFFFu : (s_union[lb >> 1] >> (16 * (lb & 1))) & 0xFFFFu;
-                const uint8_t *unit = FMT == AS_FP4_NV ? wslice + (size_t)b * df_unit(FMT)
-                                                       : wslice + (size_t)(b >> 1) * df_unit(FMT) + (b & 1) * 1024;
-                const uint32_t dst = ring + (uint32_t)(s % DF_DEPTH) * DF_STAGE;
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if ((keep >> (4 * q4 + r)) & 1u) cp_async8(dst + r * 256 + lane * 8, unit + r * 256 + q4 * 64 + g8 * 8);
-                const uint8_t *sc = FMT == AS_FP4_NV ? unit + 1024
-                                                     : wslice + (size_t)(b >> 1) * df_unit(FMT) + 2048;
-                if (lane < 8) cp_async16(dst + 1024 + lane * 16, sc + lane * 16, 16u);
-            }
-            cp_async_commit();
-        };
-        // every channel is wanted: the stream does not depend on the selection.
-        // The select kernel lets this one start after its own wait, so all
-        // work before it in the stream, the weights among it, is complete.
-        if (a.stream_all && (a.after_select || waited)) {
-#pragma unroll
-            for (int s = 0; s < DF_DEPTH - 1; ++s) issue(s, true);
-        }
-        if (!waited) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            waited = true;
-            if (a.stream_all && !a.after_select) {
-#pragma unroll
-                for (int s = 0; s < DF_DEPTH - 1; ++s) issue(s, true);
-            }
-            if (tid < TP) s_eta[tid] = (a.eta && tid < T) ? a.eta[tid] : 0.0f;
-        }
+        const int nw = min(C::KSUB / 32, w1 - ws), mine = steps_of(ws);
+        if (a.stream_all && ws > w0) prologue(ws, true);
         for (int w = tid; w < nw; w += DF_THREADS) {
             uint32_t u = 0;
 #pragma unroll
@@ -272,31 +319,27 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
             s_union[w] = u;
         }
         __syncthreads();
-        if (!a.stream_all) {
-#pragma unroll
-            for (int s = 0; s < DF_DEPTH - 1; ++s) issue(s, false);
-        }
-        // kept values, in PARTS bf16 parts: v = p0 + p1 + p2, each the
-        // rounding of what the ones before left
+        if (!a.stream_all) prologue(ws, false);
+        // kept values, scaled, in PARTS f16 parts, each the rounding of what
+        // the one before left
         const int groups = 4 * nw;
         for (int i = tid; i < TP * groups; i += DF_THREADS) {
             const int t = i / groups, g = i % groups;
             float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             const uint32_t keep = (s_keep[t][g >> 2] >> (8 * (g & 3))) & 0xFFu;
             if (t < T && keep && as_in((long long)t * K + 32 * ws + 8 * g + 7, (long long)T * K)) {
-                const size_t at = (size_t)t * K + 32 * (size_t)ws + 8 * (size_t)g;
-                if (a.bf16) load8(static_cast<const __nv_bfloat16 *>(a.x) + at, v);
-                else load8(static_cast<const float *>(a.x) + at, v);
-                const float eta = s_eta[t];
+                load_x(t, 32 * ws + 8 * g, v);
+                const float eta = s_eta[t], mul = s_mul[t];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = (keep >> e) & 1u ? (a.eta ? __fsub_rn(v[e], eta) : v[e]) : 0.0f;
+                for (int e = 0; e < 8; ++e)
+                    v[e] = (keep >> e) & 1u ? __fmul_rn(a.eta ? __fsub_rn(v[e], eta) : v[e], mul) : 0.0f;
             }
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                    const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
                     w[k] = *reinterpret_cast<const uint32_t *>(&h);
                     if (p + 1 < PARTS) {  // nothing is left of an infinity
                         const float h0 = __low2float(h), h1 = __high2float(h);
@@ -321,7 +364,7 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
             uint32_t sc[4];
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(sc[0]), "=r"(sc[1]), "=r"(sc[2]), "=r"(sc[3]) : "r"(src + 1024 + g8 * 16) : "memory");
-            issue(s + DF_DEPTH - 1, a.stream_all);
+            issue(ws, s + DF_DEPTH - 1, mine, a.stream_all);
             uint32_t bx[NT][PARTS][2];
             const int cl = 16 * (DF_WARPS * s + warp) + 4 * q4;
 #pragma unroll
@@ -333,48 +376,41 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
                     bx[n][p][1] = v.y;
                 }
 #pragma unroll
-            for (int wd = 0; wd < 2; ++wd)
+            for (int wd = 0; wd < 2; ++wd) {
+                // codes of a channel pair in one byte: outputs p = 8 wd + 2 b
+                // (lo, byte b) and p + 1 (hi), channels 4q, 4q+1 | 4q+2, 4q+3
+                uint32_t A[4][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t sel = h ? 0x7632u : 0x5410u;
-                    const uint32_t X[2] = {__byte_perm(wv[0][wd], wv[1][wd], sel), __byte_perm(wv[2][wd], wv[3][wd], sel)};
-                    uint32_t A[4][2];  // code j, channel pair
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        A[0][k] = X[k] & 0x81C081C0u;
-                        A[1][k] = ((X[k] >> 3) & 0x01C001C0u) | ((X[k] << 1) & 0x80008000u);
-                        A[2][k] = ((X[k] << 6) & 0x01C001C0u) | ((X[k] << 2) & 0x80008000u);
-                        A[3][k] = (X[k] << 3) & 0x81C081C0u;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int p = wd * 8 + h * 4 + j;
-                        const uint32_t dup = __byte_perm(sc[p >> 2], 0u, 0x4040u | (uint32_t)(p & 3) | ((uint32_t)(p & 3) << 8));
-                        // byte in bits 0..7 and 16..23
-                        const uint32_t s2 = FMT == AS_FP4_NV ? dup * 16u + 0x70007000u : dup * 128u;
-                        A[j][0] = bf16x2_mul(A[j][0], s2);
-                        A[j][1] = bf16x2_mul(A[j][1], s2);
-                    }
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int p = 0; p < PARTS; ++p)
-                                mma_16816(acc[wd * 4 + h * 2 + m][n], A[2 * m][0], A[2 * m + 1][0], A[2 * m][1],
-                                          A[2 * m + 1][1], bx[n][p][0], bx[n][p][1]);
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t x0 = wv[2 * k][wd], x1 = wv[2 * k + 1][wd];
+                    e2m1x8((x0 & 0x0F0F0F0Fu) | ((x1 << 4) & 0xF0F0F0F0u), A[2 * k]);
+                    e2m1x8(((x0 >> 4) & 0x0F0F0F0Fu) | (x1 & 0xF0F0F0F0u), A[2 * k + 1]);
                 }
+                float f[8];
+                df_scales<FMT>(sc[2 * wd], *reinterpret_cast<float (*)[4]>(f));
+                df_scales<FMT>(sc[2 * wd + 1], *reinterpret_cast<float (*)[4]>(f + 4));
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int p = PARTS - 1; p >= 0; --p)  // the small part first
+                            mma_f16(d, A[0][b], A[1][b], A[2][b], A[3][b], bx[n][p][0], bx[n][p][1], d);
+                        float (&o)[4] = acc[4 * wd + b][n];
+                        o[0] = fmaf(f[2 * b], d[0], o[0]);
+                        o[1] = fmaf(f[2 * b], d[1], o[1]);
+                        o[2] = fmaf(f[2 * b + 1], d[2], o[2]);
+                        o[3] = fmaf(f[2 * b + 1], d[3], o[3]);
+                    }
+            }
         }
         cp_async_wait<0>();
         __syncthreads();  // x and the ring are free
     }
-    if (!waited) {  // a rank without channels
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (tid < TP) s_eta[tid] = (a.eta && tid < T) ? a.eta[tid] : 0.0f;
-        __syncthreads();
-    }
 
     // warps in order, then the cluster's CTAs in order
+    __syncthreads();
 #pragma unroll
     for (int m = 0; m < 8; ++m)
 #pragma unroll
@@ -387,11 +423,11 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
         }
     __syncthreads();
     for (int i = tid; i < T * DF_COLS; i += DF_THREADS) {
-        const int at = (i / DF_COLS) * DF_RSTRIDE + i % DF_COLS;
+        const int t = i / DF_COLS, at = t * DF_RSTRIDE + i % DF_COLS;
         float s = red[at];
 #pragma unroll
         for (int w = 1; w < DF_WARPS; ++w) s += red[w * TP * DF_RSTRIDE + at];
-        red[at] = s;
+        red[at] = s * s_inv[t];
     }
     cluster_sync_all();
     for (int i = rank * DF_THREADS + tid; i < T * DF_COLS; i += nranks * DF_THREADS) {
@@ -447,11 +483,8 @@ static cudaError_t launch_df(const DecodeFp4Args &a, cudaStream_t st)
 template <int NT, int FMT>
 static cudaError_t launch_df_parts(const DecodeFp4Args &a, cudaStream_t st)
 {
-    // kept values: bf16 x without a shift is one bf16 part exactly; else
-    // three parts hold a float32 (24 bits) exactly, and two are within 2^-17,
-    // far inside the half step (2^-9) of a bf16 output
-    if (a.bf16 && !a.eta) return launch_df<NT, 1, FMT>(a, st);
-    return a.out_bf16 ? launch_df<NT, 2, FMT>(a, st) : launch_df<NT, 3, FMT>(a, st);
+    // a bf16 value without a shift fits one f16 part
+    return a.bf16 && !a.eta ? launch_df<NT, 1, FMT>(a, st) : launch_df<NT, 2, FMT>(a, st);
 }
 
 cudaError_t launch_decode_fp4(DecodeFp4Args a, int fmt, cudaStream_t st)
