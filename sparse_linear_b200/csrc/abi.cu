@@ -57,10 +57,8 @@ size_t decode_ws(int T, int K, int n_out, const as_config *cfg, int bf16)
 
 size_t decode_fp4_ws(int T, int K, const as_config *cfg)
 {
-    size_t bytes = round_up((size_t)T * ((K + 31) / 32) * sizeof(uint32_t), 256) +
-                   round_up((size_t)T * sizeof(float), 256);
-    if (cfg->score == AS_SCORE_CLACT) bytes += round_up(colnorm_workspace(T, K), 256);
-    return bytes;
+    return decode_fp4_layout(T, K).bytes +
+           (cfg->score == AS_SCORE_CLACT ? round_up(colnorm_workspace(T, K), 256) : 0);
 }
 
 size_t select_ws(int T, int K, const as_config *cfg)
@@ -682,52 +680,43 @@ extern "C" as_status as_linear_decode_fp4(const void *x, as_dtype dt, int T, int
     if (!aligned16(workspace)) return AS_ERR_ALIGN;
     if (!workspace || ws_bytes < decode_fp4_ws(T, K, cfg)) return AS_ERR_WORKSPACE;
     const int bf16 = dt == AS_BF16;
+    const DecodeFp4Layout lay = decode_fp4_layout(T, K);
     char *ws = static_cast<char *>(workspace);
-    uint32_t *mask = mask_out ? mask_out : reinterpret_cast<uint32_t *>(ws);
-    ws += round_up((size_t)T * ((K + 31) / 32) * sizeof(uint32_t), 256);
-    float *eta = eta_out ? eta_out : reinterpret_cast<float *>(ws);
-    ws += round_up((size_t)T * sizeof(float), 256);
 
-    DecodeFp4Args a{};
-    // keep-all without a shift or a mask to report needs no selection kernel
-    const bool select = cfg->sel != AS_SEL_ALL || cfg->dpts || mask_out;
-    const float *f = cfg->score == AS_SCORE_WEIGHT ? g : nullptr;
-    if (cfg->score == AS_SCORE_CLACT && (select || colnorm_out)) {
+    SelectArgs s{};
+    s.x = x;
+    s.bf16 = bf16;
+    s.T = T;
+    s.K = K;
+    s.score = cfg->score;
+    s.sel = cfg->sel;
+    s.n = cfg->n;
+    s.m = cfg->m;
+    s.k_keep = cfg->k_keep;
+    s.dpts = cfg->dpts;
+    s.tau = cfg->tau;
+    s.eta_static = cfg->dpts == AS_PTS_STATIC ? cfg->eta_static : nullptr;
+    s.f = cfg->score == AS_SCORE_WEIGHT ? g : nullptr;
+    s.bitmask = mask_out ? mask_out : reinterpret_cast<uint32_t *>(ws);
+    s.eta = cfg->dpts ? (eta_out ? eta_out : reinterpret_cast<float *>(ws + lay.eta)) : nullptr;
+    if (cfg->score == AS_SCORE_CLACT) {
+        char *cw = ws + lay.bytes;
         float *c = colnorm_out;
-        if (!c) c = reinterpret_cast<float *>(ws + colnorm_workspace(T, K) - (size_t)K * sizeof(float));
-        if (launch_colnorm(x, bf16, T, K, c, ws, stream) != cudaSuccess) return AS_ERR_CUDA;
-        f = c;
+        if (!c) c = reinterpret_cast<float *>(cw + colnorm_workspace(T, K) - (size_t)K * sizeof(float));
+        if (launch_colnorm(x, bf16, T, K, c, cw, stream) != cudaSuccess) return AS_ERR_CUDA;
+        s.f = c;
     }
-    if (select) {
-        SelectArgs s{};
-        s.x = x;
-        s.bf16 = bf16;
-        s.T = T;
-        s.K = K;
-        s.score = cfg->score;
-        s.sel = cfg->sel;
-        s.n = cfg->n;
-        s.m = cfg->m;
-        s.k_keep = cfg->k_keep;
-        s.dpts = cfg->dpts;
-        s.tau = cfg->tau;
-        s.eta_static = cfg->dpts == AS_PTS_STATIC ? cfg->eta_static : nullptr;
-        s.f = f;
-        s.bitmask = mask;
-        s.eta = cfg->dpts ? eta : nullptr;
-        const cudaError_t se = (cfg->sel == AS_SEL_NM && bf16) ? launch_select_nm_decode(s, stream)
-                                                               : launch_select(s, stream, /*wide=*/1);
-        if (se != cudaSuccess) return AS_ERR_CUDA;
-        a.mask = mask;
-        a.after_select = 1;
-    }
+    const bool topk = cfg->sel == AS_SEL_TOPK;  // needs the whole row's scores: a kernel of its own
+    if (topk && launch_select(s, stream, /*wide=*/1) != cudaSuccess) return AS_ERR_CUDA;
+    DecodeFp4Args a{};
     a.x = x;
     a.bf16 = bf16;
     a.T = T;
     a.K = K;
     a.n_out = n_out;
     a.Wd = Wd;
-    a.eta = cfg->dpts ? eta : nullptr;
+    a.mask = s.bitmask;
+    a.eta = s.eta;
     a.rowsum = rowsum;
     a.y = y;
     a.out_bf16 = cfg->out_dtype == AS_BF16;
@@ -738,8 +727,8 @@ extern "C" as_status as_linear_decode_fp4(const void *x, as_dtype dt, int T, int
     d.n = cfg->n;
     d.m = cfg->m;
     d.k_keep = cfg->k_keep;
-    a.stream_all = !select || decode_streams_all(d);
-    return cuda_status(launch_decode_fp4(a, fmt, stream));
+    a.stream_all = decode_streams_all(d);
+    return cuda_status(launch_decode_fp4(a, s, topk, workspace, fmt, stream));
 }
 
 // Validation and GEMM arguments shared by the prefill entry points.

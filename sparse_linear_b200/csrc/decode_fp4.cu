@@ -17,9 +17,12 @@
 //   row's largest; a float32 factor per output carries that power of two and
 //   the weight's row scale.
 //   Kept values enter as one or two f16 parts after scaling each token by a
-//   power of two that puts its largest |x| in the CTA's range of K at 2^14: bf16
-//   values are exact from 2^-28 of the largest up, smaller ones err by at most
-//   2^-39 of it; two parts hold 22 bits of a float32 value.
+//   power of two that puts its largest |x| at 2^14: bf16 values are exact from
+//   2^-28 of the largest up, smaller ones err by at most 2^-39 of it; two parts
+//   hold 22 bits of a float32 value.
+//
+// Kernels of a call: (top-k: the selection kernel,) k_fp4_stage, k_decode_fp4,
+// chained by programmatic dependent launch.
 #include "common.cuh"
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -30,8 +33,7 @@ namespace as {
 constexpr int DF_COLS = 128;     // output columns per slice
 constexpr int DF_WARPS = 8;
 constexpr int DF_THREADS = DF_WARPS * 32;
-constexpr int DF_DEPTH = 8;      // 16-channel steps in flight per warp
-constexpr int DF_STAGE = 1024 + 128;
+constexpr int DF_CODES = 1024 + 128;  // bytes of a 16-channel step: codes and scales
 constexpr int DF_RSTRIDE = DF_COLS + 4;  // padded row of the reduction buffer (no bank conflicts)
 
 __host__ __device__ constexpr int df_unit(int fmt) { return fp4_block(fmt) * 64 + 128; }
@@ -127,26 +129,153 @@ cudaError_t launch_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const
     return cudaGetLastError();
 }
 
+// ------------------------------------------------------------------ staging
+// Grid (token, 2048-channel chunk).  Every CTA of a token reads the whole row
+// (the same code and order as k_select_nm_decode: identical bits) for the mean
+// and the largest |x|, selects its own channels (or takes a mask) and writes
+// the keep words and the kept values as f16 parts, in the order the decode
+// reads them: [16-channel step][part][token of TP][16].  Rows of tokens past T
+// are not written: they only reach output columns past T.
+constexpr int DS_THREADS = 256;
+constexpr int DS_CHUNK = DS_THREADS * 8;
+constexpr int DS_ROWREG = 8;  // row loads in flight per thread
+
+struct StageArgs {
+    const void *x;
+    int T, K, TP;
+    int score_f, sel, n, m, dpts;  // score_f: multiply |x| by f
+    float tau;
+    const float *eta_static, *f;
+    const uint32_t *mask_in;  // selection made before, with its eta in eta_in; or nullptr
+    const float *eta_in;
+    uint32_t *mask;  // keep words, written unless mask_in
+    float *eta;      // [T], written unless mask_in (with a shift)
+    float *inv;      // [T] power of two that undoes the scaling
+    __half *xh;
+};
+
+template <typename TX, int PARTS>
+__global__ void __launch_bounds__(DS_THREADS) k_fp4_stage(StageArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // after the wait: see k_select_nm_decode
+    __shared__ double red[DS_THREADS / 32];
+    __shared__ uint32_t redm[DS_THREADS / 32];
+    const int t = blockIdx.x, chunk = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int K = a.K, ng = K >> 3, words = (K + 31) >> 5;
+    const TX *xr = static_cast<const TX *>(a.x) + (size_t)t * K;
+    const int c0 = chunk * DS_CHUNK + warp * 256 + 8 * lane;  // this lane's 8 channels
+    const bool act = c0 < K;
+
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, f[8];
+    if (act) load8(xr + c0, v);
+    const bool has_f = a.score_f && act && !a.mask_in;
+    if (has_f) load8f(a.f + c0, f);
+    uint32_t word = 0xFFFFFFFFu;
+    if (a.mask_in && act) word = a.mask_in[(size_t)t * words + (c0 >> 5)];
+    float eta = !a.dpts ? 0.0f : (a.mask_in ? a.eta_in[t] : (a.dpts == AS_PTS_STATIC ? a.eta_static[t] : 0.0f));
+    const bool mean = a.dpts == AS_PTS_DYNAMIC && !a.mask_in;
+
+    double sum = 0.0;
+    uint32_t top = 0;  // largest finite |x| (bits)
+    for (int g0 = 0; g0 < ng; g0 += DS_ROWREG * DS_THREADS) {
+        float w[DS_ROWREG][8];
+#pragma unroll
+        for (int r = 0; r < DS_ROWREG; ++r) {
+            const int g = g0 + tid + r * DS_THREADS;
+            if (g < ng) load8(xr + 8 * (size_t)g, w[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < DS_ROWREG; ++r) {
+            const int g = g0 + tid + r * DS_THREADS;
+            if (g < ng) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (mean) sum += (double)w[r][e];
+                    const uint32_t b = __float_as_uint(w[r][e]) & 0x7FFFFFFFu;
+                    top = max(top, b < F32_INF_BITS ? b : 0u);
+                }
+            }
+        }
+    }
+    if (mean) {
+        sum = warp_sum_f64(sum);
+        if (lane == 0) red[warp] = sum;
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) redm[warp] = top;
+    __syncthreads();
+    if (mean) {
+        double tot = 0.0;
+#pragma unroll
+        for (int w = 0; w < DS_THREADS / 32; ++w) tot += red[w];
+        eta = (float)(tot / (double)K);
+    }
+#pragma unroll
+    for (int w = 0; w < DS_THREADS / 32; ++w) top = max(top, redm[w]);
+    const uint32_t bound = __float_as_uint(__uint_as_float(top) + fabsf(eta));  // |x - eta| is at most this
+    int e = bound == 0u ? 0 : 14 - ((int)(bound >> 23) - 127);
+    e = e > 126 ? 126 : (e < -113 ? -113 : e);
+    if (chunk == 0 && tid == 0) {
+        a.inv[t] = pow2f(-e);
+        if (a.dpts && !a.mask_in) a.eta[t] = eta;
+    }
+    float xh[8], sc[8];
+    score8(v, a.dpts, eta, has_f ? f : nullptr, 0, xh, sc);
+    uint32_t keep;
+    if (a.mask_in) {
+        keep = (word >> (8 * (lane & 3))) & 0xFFu;
+    } else {
+        keep = a.sel == AS_SEL_NM ? nm_keep_dispatch(sc, lane, a.n, a.m)
+                                  : (a.sel == AS_SEL_THRESH ? keep_thresh(sc, a.tau) : 0xFFu);
+        if (!act) keep = 0;
+        word = keep << (8 * (lane & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, 1);
+        word |= __shfl_xor_sync(0xffffffffu, word, 2);
+        const int wi = c0 >> 5;
+        if ((lane & 3) == 0 && act && as_in((long long)t * words + wi, (long long)a.T * words))
+            a.mask[(size_t)t * words + wi] = word;
+    }
+    if (!act) return;
+    // two or one f16 parts, the second the rounding of what the first left
+    const float mul = pow2f(e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) xh[k] = (keep >> k) & 1u ? __fmul_rn(xh[k], mul) : 0.0f;
+    __half *out = a.xh + ((size_t)(c0 >> 4) * PARTS * a.TP + t) * 16 + (c0 & 8);
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __half2 h = __floats2half2_rn(xh[2 * k], xh[2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t *>(&h);
+            if (p + 1 < PARTS) {  // nothing is left of an infinity
+                const float h0 = __low2float(h), h1 = __high2float(h);
+                xh[2 * k] = isinf(h0) ? 0.0f : xh[2 * k] - h0;
+                xh[2 * k + 1] = isinf(h1) ? 0.0f : xh[2 * k + 1] - h1;
+            }
+        }
+        *reinterpret_cast<uint4 *>(out + (size_t)p * a.TP * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 // ------------------------------------------------------------------ decode
 // CTA (rank of a cluster, slice): the slice's 128 columns and a contiguous
-// part of K; its warps take 16-channel steps in turn.  A lane copies its own
-// pieces of the kept rows (cp.async, a ring of its own in shared memory),
-// turns them into A fragments and multiplies with the kept values of x, which
-// the CTA stages in shared memory as PARTS f16 arrays (zero where a token
-// dropped the channel, so rows that were not loaded do not matter).  The
-// warps' sums are added in shared memory and the cluster's through
-// distributed shared memory, both in a fixed order.
+// part of K; its warps take 16-channel steps in turn, each with a cp.async
+// ring of its own (codes of kept rows, scales, staged x of a step).  Rows that
+// no token keeps are not loaded: their kept values are zero and a code is
+// finite whatever its bits.  The warps' sums are added in shared memory and
+// the cluster's through distributed shared memory, both in a fixed order.
 template <int NT, int PARTS>
 struct DfCfg {
     static constexpr int TP = 8 * NT;
-    static constexpr int KSUB = NT * PARTS <= 2 ? 2048 : 1024;  // channels of x staged at a time
-    static constexpr int XS = KSUB + 16;                        // row stride: token rows 8 banks apart
-    static constexpr size_t xbytes = (size_t)PARTS * TP * XS * 2;
-    static constexpr size_t ring = (size_t)DF_WARPS * DF_DEPTH * DF_STAGE;
+    static constexpr int XB = PARTS * TP * 32;       // staged x of a step, bytes
+    static constexpr int STAGE = DF_CODES + XB;
+    static constexpr int DEPTH = NT * PARTS == 4 ? 6 : 8;  // steps in flight per warp: two CTAs per SM fit
+    static constexpr size_t ring = (size_t)DF_WARPS * DEPTH * STAGE;
     static constexpr size_t red = (size_t)DF_WARPS * TP * DF_RSTRIDE * 4;
-    static constexpr size_t big = ring > red ? ring : red;
-    static constexpr size_t smem = big + xbytes;
-    static constexpr int per_sm = smem <= 110 * 1024 ? 2 : 1;
+    static constexpr size_t smem = ring > red ? ring : red;
 };
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
@@ -154,11 +283,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
-}
-
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // Four bytes of two codes each -> four f16x2.
@@ -174,14 +298,22 @@ __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&r)[4])
         : "r"(w));
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1, const float (&c)[4])
+// D = A B and D += A B.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%10,%11,%12,%13};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_f16_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // The scales of outputs p (bytes of sc) as float32.
@@ -201,18 +333,16 @@ __device__ __forceinline__ void df_scales(uint32_t sc, float (&f)[4])
     }
 }
 
+constexpr int DF_MAXW = 1024;  // keep words of a CTA's range held in shared memory
+
 template <int NT, int PARTS, int FMT>
-__global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode_fp4(DecodeFp4Args a)
+__global__ void __launch_bounds__(DF_THREADS, 2) k_decode_fp4(DecodeFp4Args a)
 {
     using C = DfCfg<NT, PARTS>;
-    constexpr int TP = C::TP;
+    constexpr int TP = C::TP, DEPTH = C::DEPTH;
     extern __shared__ __align__(16) unsigned char smem[];
     float *red = reinterpret_cast<float *>(smem);  // after the main loop
-    __half *xs = reinterpret_cast<__half *>(smem + C::big);
-    __shared__ uint32_t s_keep[TP][C::KSUB / 32];
-    __shared__ uint32_t s_union[C::KSUB / 32];
-    __shared__ float s_eta[TP], s_mul[TP], s_inv[TP];  // shift; power of two into and out of f16's range
-    __shared__ uint32_t s_max[TP];
+    __shared__ uint32_t s_union[DF_MAXW];
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, q4 = lane & 3;
@@ -221,76 +351,63 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
     const int nwords = K >> 5, wper = (nwords + nranks - 1) / nranks;
     const int w0 = min(nwords, rank * wper), w1 = min(nwords, w0 + wper);
     const uint8_t *wslice = a.Wd + (size_t)slice * (size_t)(K / fp4_block(FMT)) * df_unit(FMT);
-    const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (DF_DEPTH * DF_STAGE);
+    const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (DEPTH * C::STAGE);
+    // step s of this warp: channels 32 w0 + 16 (DF_WARPS s + warp) ..
+    const int nsteps = 2 * (w1 - w0);
+    const int mine = nsteps > warp ? (nsteps - warp + DF_WARPS - 1) / DF_WARPS : 0;
+    const uint8_t *xsrc = reinterpret_cast<const uint8_t *>(a.xh) + (size_t)(2 * w0) * C::XB;
+    // 16-byte piece `lane` (and lane + 32) of the 16 rows: row 4r + q of channel 4q + r
+    const int bit0 = 4 * ((lane >> 2) & 3) + (lane >> 4), bit1 = bit0 + 2;
 
-    // step s of this warp in the part that starts at word ws covers channels
-    // 32 ws + 16 (DF_WARPS s + warp); it has `mine` of them
-    auto steps_of = [&](int ws) {
-        const int n = 2 * min(C::KSUB / 32, w1 - ws);
-        return n > warp ? (n - warp + DF_WARPS - 1) / DF_WARPS : 0;
+    auto issue_codes = [&](int s, uint32_t keep) {
+        const int b = 2 * w0 + DF_WARPS * s + warp;
+        const uint8_t *unit = FMT == AS_FP4_NV ? wslice + (size_t)b * df_unit(FMT)
+                                               : wslice + (size_t)(b >> 1) * df_unit(FMT) + (b & 1) * 1024;
+        const uint8_t *sc = FMT == AS_FP4_NV ? unit + 1024 : wslice + (size_t)(b >> 1) * df_unit(FMT) + 2048;
+        const uint32_t dst = ring + (uint32_t)(s % DEPTH) * C::STAGE + 16 * lane;
+        if ((keep >> bit0) & 1u) cp_async16(dst, unit + 16 * lane, 16u);
+        if ((keep >> bit1) & 1u) cp_async16(dst + 512, unit + 512 + 16 * lane, 16u);
+        if (lane < 8) cp_async16(dst + 1024, sc + 16 * lane, 16u);
     };
-    auto issue = [&](int ws, int s, int mine, bool all) {
-        if (s < mine) {
-            const int lb = DF_WARPS * s + warp, b = 2 * ws + lb;
-            const uint32_t keep = all ? 0xFFFFu : (s_union[lb >> 1] >> (16 * (lb & 1))) & 0xFFFFu;
-            const uint8_t *unit = FMT == AS_FP4_NV ? wslice + (size_t)b * df_unit(FMT)
-                                                   : wslice + (size_t)(b >> 1) * df_unit(FMT) + (b & 1) * 1024;
-            const uint32_t dst = ring + (uint32_t)(s % DF_DEPTH) * DF_STAGE;
+    auto issue_x = [&](int s) {
+        const uint8_t *src = xsrc + (size_t)(DF_WARPS * s + warp) * C::XB + 16 * lane;
+        const uint32_t dst = ring + (uint32_t)(s % DEPTH) * C::STAGE + DF_CODES + 16 * lane;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if ((keep >> (4 * q4 + r)) & 1u) cp_async8(dst + r * 256 + lane * 8, unit + r * 256 + q4 * 64 + g8 * 8);
-            const uint8_t *sc = FMT == AS_FP4_NV ? unit + 1024 : wslice + (size_t)(b >> 1) * df_unit(FMT) + 2048;
-            if (lane < 8) cp_async16(dst + 1024 + lane * 16, sc + lane * 16, 16u);
-        }
-        cp_async_commit();
+        for (int i = 0; i < (C::XB + 511) / 512; ++i)
+            if (512 * i + 16 * lane < C::XB) cp_async16(dst + 512 * i, src + 512 * i, 16u);
     };
-    auto prologue = [&](int ws, bool all) {
-        const int mine = steps_of(ws);
-#pragma unroll
-        for (int s = 0; s < DF_DEPTH - 1; ++s) issue(ws, s, mine, all);
-    };
-    auto load_x = [&](int t, int c, float (&v)[8]) {  // channels c .. c+7 of token t
-        const size_t at = (size_t)t * K + (size_t)c;
-        if (a.bf16) load8(static_cast<const __nv_bfloat16 *>(a.x) + at, v);
-        else load8(static_cast<const float *>(a.x) + at, v);
+    auto kept_rows = [&](int s) -> uint32_t {
+        if (a.stream_all) return 0xFFFFu;
+        const int lb = DF_WARPS * s + warp, w = lb >> 1;
+        uint32_t u = w < DF_MAXW ? s_union[w] : 0xFFFFFFFFu;
+        return (u >> (16 * (lb & 1))) & 0xFFFFu;
     };
 
-    // The select kernel lets this one start after its own wait, so everything
-    // before that kernel in the stream (x and the weights) is complete.  What
-    // does not depend on the selection comes before the wait for it: the
-    // tokens' largest |x| and, if every channel is wanted, the first weights.
-    if (!a.after_select) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (a.stream_all) prologue(w0, true);
-    if (tid < TP) s_max[tid] = 0u;
-    __syncthreads();
-    {
-        const int tiles = (w1 - w0 + 7) >> 3;  // 256 channels
-        for (int i = warp; i < T * tiles; i += DF_WARPS) {
-            const int t = i / tiles, c = 32 * w0 + 256 * (i % tiles) + 8 * lane;
-            uint32_t m = 0;
-            if (c < 32 * w1 && as_in((long long)t * K + c + 7, (long long)T * K)) {
-                float v[8];
-                load_x(t, c, v);
+    // The staging kernel lets this one start after its own wait, so everything
+    // before that kernel in the stream (the weights among it) is complete: if
+    // every channel is wanted, the codes of the first steps come before the
+    // wait for the staged x.
+    if (a.stream_all)
+        for (int s = 0; s < DEPTH - 1; ++s)
+            if (s < mine) issue_codes(s, 0xFFFFu);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!a.stream_all) {
+        for (int w = tid; w < min(w1 - w0, DF_MAXW); w += DF_THREADS) {
+            uint32_t u = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t b = __float_as_uint(v[e]) & 0x7FFFFFFFu;
-                    m = max(m, b < F32_INF_BITS ? b : 0u);
-                }
-            }
-            m = __reduce_max_sync(0xffffffffu, m);
-            if (lane == 0) atomicMax(&s_max[t], m);
+            for (int t = 0; t < TP; ++t)
+                if (t < T && as_in((long long)t * nwords + w0 + w, (long long)T * nwords))
+                    u |= a.mask[(size_t)t * nwords + w0 + w];
+            s_union[w] = u;
         }
+        __syncthreads();
     }
-    __syncthreads();
-    if (a.after_select) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tid < TP) {
-        const float eta = (a.eta && tid < T) ? a.eta[tid] : 0.0f;
-        s_eta[tid] = eta;
-        const uint32_t top = __float_as_uint(__uint_as_float(s_max[tid]) + fabsf(eta));  // bounds |x - eta|
-        int e = top == 0u ? 0 : 14 - ((int)(top >> 23) - 127);
-        e = e > 126 ? 126 : (e < -113 ? -113 : e);
-        s_mul[tid] = pow2f(e);
-        s_inv[tid] = pow2f(-e);
+    for (int s = 0; s < DEPTH - 1; ++s) {
+        if (s < mine) {
+            if (!a.stream_all) issue_codes(s, kept_rows(s));
+            issue_x(s);
+        }
+        cp_async_commit();  // with stream_all the first group also holds the codes before the wait
     }
 
     float acc[8][NT][4];
@@ -301,113 +418,61 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
 
-    for (int ws = w0; ws < w1; ws += C::KSUB / 32) {
-        const int nw = min(C::KSUB / 32, w1 - ws), mine = steps_of(ws);
-        if (a.stream_all && ws > w0) prologue(ws, true);
-        for (int w = tid; w < nw; w += DF_THREADS) {
-            uint32_t u = 0;
+    for (int s = 0; s < mine; ++s) {
+        cp_async_wait<DEPTH - 2>();
+        __syncwarp();  // a step's pieces were copied by all lanes
+        const uint32_t src = ring + (uint32_t)(s % DEPTH) * C::STAGE;
+        uint32_t wv[4][2];
 #pragma unroll
-            for (int t = 0; t < TP; ++t) {
-                uint32_t k = 0u;
-                if (t < T)
-                    k = !a.mask ? 0xFFFFFFFFu
-                                : (as_in((long long)t * nwords + ws + w, (long long)T * nwords)
-                                       ? a.mask[(size_t)t * nwords + ws + w] : 0u);
-                s_keep[t][w] = k;
-                u |= k;
-            }
-            s_union[w] = u;
+        for (int r = 0; r < 4; ++r)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wv[r][0]), "=r"(wv[r][1])
+                         : "r"(src + r * 256 + q4 * 64 + g8 * 8) : "memory");
+        uint32_t sc[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(sc[0]), "=r"(sc[1]), "=r"(sc[2]), "=r"(sc[3]) : "r"(src + 1024 + g8 * 16) : "memory");
+        uint32_t bx[NT][PARTS][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p)
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(bx[n][p][0]), "=r"(bx[n][p][1])
+                             : "r"(src + DF_CODES + (p * TP + 8 * n + g8) * 32 + q4 * 8) : "memory");
+        if (s + DEPTH - 1 < mine) {  // into the slot read at s - 1
+            issue_codes(s + DEPTH - 1, kept_rows(s + DEPTH - 1));
+            issue_x(s + DEPTH - 1);
         }
-        __syncthreads();
-        if (!a.stream_all) prologue(ws, false);
-        // kept values, scaled, in PARTS f16 parts, each the rounding of what
-        // the one before left
-        const int groups = 4 * nw;
-        for (int i = tid; i < TP * groups; i += DF_THREADS) {
-            const int t = i / groups, g = i % groups;
-            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            const uint32_t keep = (s_keep[t][g >> 2] >> (8 * (g & 3))) & 0xFFu;
-            if (t < T && keep && as_in((long long)t * K + 32 * ws + 8 * g + 7, (long long)T * K)) {
-                load_x(t, 32 * ws + 8 * g, v);
-                const float eta = s_eta[t], mul = s_mul[t];
+        cp_async_commit();
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = (keep >> e) & 1u ? __fmul_rn(a.eta ? __fsub_rn(v[e], eta) : v[e], mul) : 0.0f;
+        for (int wd = 0; wd < 2; ++wd) {
+            // codes of a channel pair in one byte: outputs p = 8 wd + 2 b (A[0],
+            // A[2], byte b) and p + 1 (A[1], A[3]); channels 4q, 4q+1 | 4q+2, 4q+3
+            uint32_t A[4][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t x0 = wv[2 * k][wd], x1 = wv[2 * k + 1][wd];
+                e2m1x8((x0 & 0x0F0F0F0Fu) | ((x1 << 4) & 0xF0F0F0F0u), A[2 * k]);
+                e2m1x8(((x0 >> 4) & 0x0F0F0F0Fu) | (x1 & 0xF0F0F0F0u), A[2 * k + 1]);
             }
+            float f[2][4];
+            df_scales<FMT>(sc[2 * wd], f[0]);
+            df_scales<FMT>(sc[2 * wd + 1], f[1]);
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-                uint32_t w[4];
+            for (int b = 0; b < 4; ++b)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
-                    w[k] = *reinterpret_cast<const uint32_t *>(&h);
-                    if (p + 1 < PARTS) {  // nothing is left of an infinity
-                        const float h0 = __low2float(h), h1 = __high2float(h);
-                        v[2 * k] = isinf(h0) ? 0.0f : v[2 * k] - h0;
-                        v[2 * k + 1] = isinf(h1) ? 0.0f : v[2 * k + 1] - h1;
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    float d[4];  // the small part first
+                    mma_f16_zero(d, A[0][b], A[1][b], A[2][b], A[3][b], bx[n][PARTS - 1][0], bx[n][PARTS - 1][1]);
+                    if constexpr (PARTS == 2) mma_f16_add(d, A[0][b], A[1][b], A[2][b], A[3][b], bx[n][0][0], bx[n][0][1]);
+                    float (&o)[4] = acc[4 * wd + b][n];
+                    const float f0 = f[b >> 1][2 * (b & 1)], f1 = f[b >> 1][2 * (b & 1) + 1];
+                    o[0] = fmaf(f0, d[0], o[0]);
+                    o[1] = fmaf(f0, d[1], o[1]);
+                    o[2] = fmaf(f1, d[2], o[2]);
+                    o[3] = fmaf(f1, d[3], o[3]);
                 }
-                *reinterpret_cast<uint4 *>(xs + ((size_t)p * TP + t) * C::XS + 8 * g) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
         }
-        __syncthreads();
-
-        for (int s = 0; s < mine; ++s) {
-            cp_async_wait<DF_DEPTH - 2>();
-            __syncwarp();  // the scale bytes were copied by other lanes
-            const uint32_t src = ring + (uint32_t)(s % DF_DEPTH) * DF_STAGE;
-            uint32_t wv[4][2];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wv[r][0]), "=r"(wv[r][1])
-                             : "r"(src + r * 256 + lane * 8) : "memory");
-            uint32_t sc[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(sc[0]), "=r"(sc[1]), "=r"(sc[2]), "=r"(sc[3]) : "r"(src + 1024 + g8 * 16) : "memory");
-            issue(ws, s + DF_DEPTH - 1, mine, a.stream_all);
-            uint32_t bx[NT][PARTS][2];
-            const int cl = 16 * (DF_WARPS * s + warp) + 4 * q4;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(xs + ((size_t)p * TP + 8 * n + g8) * C::XS + cl);
-                    bx[n][p][0] = v.x;
-                    bx[n][p][1] = v.y;
-                }
-#pragma unroll
-            for (int wd = 0; wd < 2; ++wd) {
-                // codes of a channel pair in one byte: outputs p = 8 wd + 2 b
-                // (lo, byte b) and p + 1 (hi), channels 4q, 4q+1 | 4q+2, 4q+3
-                uint32_t A[4][4];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t x0 = wv[2 * k][wd], x1 = wv[2 * k + 1][wd];
-                    e2m1x8((x0 & 0x0F0F0F0Fu) | ((x1 << 4) & 0xF0F0F0F0u), A[2 * k]);
-                    e2m1x8(((x0 >> 4) & 0x0F0F0F0Fu) | (x1 & 0xF0F0F0F0u), A[2 * k + 1]);
-                }
-                float f[8];
-                df_scales<FMT>(sc[2 * wd], *reinterpret_cast<float (*)[4]>(f));
-                df_scales<FMT>(sc[2 * wd + 1], *reinterpret_cast<float (*)[4]>(f + 4));
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int p = PARTS - 1; p >= 0; --p)  // the small part first
-                            mma_f16(d, A[0][b], A[1][b], A[2][b], A[3][b], bx[n][p][0], bx[n][p][1], d);
-                        float (&o)[4] = acc[4 * wd + b][n];
-                        o[0] = fmaf(f[2 * b], d[0], o[0]);
-                        o[1] = fmaf(f[2 * b], d[1], o[1]);
-                        o[2] = fmaf(f[2 * b + 1], d[2], o[2]);
-                        o[3] = fmaf(f[2 * b + 1], d[3], o[3]);
-                    }
-            }
-        }
-        cp_async_wait<0>();
-        __syncthreads();  // x and the ring are free
     }
+    cp_async_wait<0>();
 
     // warps in order, then the cluster's CTAs in order
     __syncthreads();
@@ -427,7 +492,7 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
         float s = red[at];
 #pragma unroll
         for (int w = 1; w < DF_WARPS; ++w) s += red[w * TP * DF_RSTRIDE + at];
-        red[at] = s * s_inv[t];
+        red[at] = s * a.inv[t];
     }
     cluster_sync_all();
     for (int i = rank * DF_THREADS + tid; i < T * DF_COLS; i += nranks * DF_THREADS) {
@@ -437,38 +502,32 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<NT, PARTS>::per_sm) k_decode
         for (int r = 0; r < nranks; ++r) s += ld_cluster_f32(mapa_u32(at, (uint32_t)r));
         if (o >= n_out || !as_in((long long)t * n_out + o, (long long)T * n_out)) continue;
         s *= a.rowf[o];
-        if (a.eta) s = fmaf(s_eta[t], a.rowsum[o], s);
+        if (a.eta) s = fmaf(a.eta[t], a.rowsum[o], s);
         if (a.out_bf16) static_cast<__nv_bfloat16 *>(a.y)[(size_t)t * n_out + o] = __float2bfloat16_rn(s);
         else static_cast<float *>(a.y)[(size_t)t * n_out + o] = s;
     }
     cluster_sync_all();  // no CTA leaves while another reads its sums
 }
 
-// CTAs of a cluster (along K): as many as fill the GPU, at least one step per
-// warp, at most the portable cluster size.
-static int df_ranks(int K, int n_out, int per_sm)
+// CTAs of a cluster (along K): as many as fill the GPU (two per SM), at least
+// one step per warp, at most the portable cluster size.
+static int df_ranks(int K, int n_out)
 {
     const int slices = (n_out + DF_COLS - 1) / DF_COLS;
-    int c = sm_count() * per_sm / slices;
+    int c = 2 * sm_count() / slices;
     const int most = K / (16 * DF_WARPS);
     if (c > most) c = most;
     return c < 1 ? 1 : (c > 8 ? 8 : c);
 }
 
-template <int NT, int PARTS, int FMT>
-static cudaError_t launch_df(const DecodeFp4Args &a, cudaStream_t st)
+static void df_launch(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid, int threads, size_t smem,
+                      int ranks, cudaStream_t st)
 {
-    using C = DfCfg<NT, PARTS>;
-    static int done[64];
-    cudaError_t e = smem_limit_once(k_decode_fp4<NT, PARTS, FMT>, C::smem, done);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    const int ranks = df_ranks(a.K, a.n_out, C::per_sm);
-    cfg.gridDim = dim3(ranks, (a.n_out + DF_COLS - 1) / DF_COLS);
-    cfg.blockDim = dim3(DF_THREADS);
-    cfg.dynamicSmemBytes = C::smem;
+    cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -476,23 +535,77 @@ static cudaError_t launch_df(const DecodeFp4Args &a, cudaStream_t st)
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = ranks > 0 ? 2 : 1;
+}
+
+template <int NT, int PARTS, int FMT>
+static cudaError_t launch_df(const DecodeFp4Args &a, const StageArgs &sa, cudaStream_t st)
+{
+    using C = DfCfg<NT, PARTS>;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    df_launch(cfg, attr, dim3(a.T, (a.K + DS_CHUNK - 1) / DS_CHUNK), DS_THREADS, 0, 0, st);
+    cudaError_t e = a.bf16 ? cudaLaunchKernelEx(&cfg, k_fp4_stage<__nv_bfloat16, PARTS>, sa)
+                           : cudaLaunchKernelEx(&cfg, k_fp4_stage<float, PARTS>, sa);
+    if (e != cudaSuccess) return e;
+    static int done[64];
+    e = smem_limit_once(k_decode_fp4<NT, PARTS, FMT>, C::smem, done);
+    if (e != cudaSuccess) return e;
+    const int ranks = df_ranks(a.K, a.n_out);
+    df_launch(cfg, attr, dim3(ranks, (a.n_out + DF_COLS - 1) / DF_COLS), DF_THREADS, C::smem, ranks, st);
     return cudaLaunchKernelEx(&cfg, k_decode_fp4<NT, PARTS, FMT>, a);
 }
 
 template <int NT, int FMT>
-static cudaError_t launch_df_parts(const DecodeFp4Args &a, cudaStream_t st)
+static cudaError_t launch_df_parts(const DecodeFp4Args &a, const StageArgs &sa, cudaStream_t st)
 {
     // a bf16 value without a shift fits one f16 part
-    return a.bf16 && !a.eta ? launch_df<NT, 1, FMT>(a, st) : launch_df<NT, 2, FMT>(a, st);
+    return a.bf16 && !a.eta ? launch_df<NT, 1, FMT>(a, sa, st) : launch_df<NT, 2, FMT>(a, sa, st);
 }
 
-cudaError_t launch_decode_fp4(DecodeFp4Args a, int fmt, cudaStream_t st)
+static int df_tpad(int T) { return T <= 8 ? 8 : 16; }
+
+// keep words, eta, scale factors, staged x (for two parts)
+DecodeFp4Layout decode_fp4_layout(int T, int K)
 {
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    DecodeFp4Layout l{};
+    l.eta = up((size_t)T * ((K + 31) / 32) * sizeof(uint32_t));
+    l.inv = l.eta + up((size_t)T * sizeof(float));
+    l.xh = l.inv + up((size_t)T * sizeof(float));
+    l.bytes = l.xh + up((size_t)K * df_tpad(T) * 2 * sizeof(__half));
+    return l;
+}
+
+cudaError_t launch_decode_fp4(DecodeFp4Args a, const SelectArgs &sel, bool selected, void *ws, int fmt, cudaStream_t st)
+{
+    const DecodeFp4Layout l = decode_fp4_layout(a.T, a.K);
+    char *w = static_cast<char *>(ws);
     a.rowf = reinterpret_cast<const float *>(a.Wd + df_codes_bytes(a.n_out, a.K, fmt));
+    a.inv = reinterpret_cast<const float *>(w + l.inv);
+    a.xh = w + l.xh;
+    StageArgs s{};
+    s.x = a.x;
+    s.T = a.T;
+    s.K = a.K;
+    s.TP = df_tpad(a.T);
+    s.score_f = sel.f != nullptr;
+    s.sel = sel.sel;
+    s.n = sel.n;
+    s.m = sel.m;
+    s.dpts = sel.dpts;
+    s.tau = sel.tau;
+    s.eta_static = sel.eta_static;
+    s.f = sel.f;
+    s.mask_in = selected ? sel.bitmask : nullptr;
+    s.eta_in = selected ? sel.eta : nullptr;
+    s.mask = sel.bitmask;
+    s.eta = sel.eta;
+    s.inv = reinterpret_cast<float *>(w + l.inv);
+    s.xh = reinterpret_cast<__half *>(w + l.xh);
     if (fmt == AS_FP4_NV)
-        return a.T <= 8 ? launch_df_parts<1, AS_FP4_NV>(a, st) : launch_df_parts<2, AS_FP4_NV>(a, st);
-    return a.T <= 8 ? launch_df_parts<1, AS_FP4_MX>(a, st) : launch_df_parts<2, AS_FP4_MX>(a, st);
+        return a.T <= 8 ? launch_df_parts<1, AS_FP4_NV>(a, s, st) : launch_df_parts<2, AS_FP4_NV>(a, s, st);
+    return a.T <= 8 ? launch_df_parts<1, AS_FP4_MX>(a, s, st) : launch_df_parts<2, AS_FP4_MX>(a, s, st);
 }
 
 }  // namespace as

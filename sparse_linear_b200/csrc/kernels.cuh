@@ -193,15 +193,24 @@ struct DecodeFp4Args {
     int T, K, n_out;
     const uint8_t *Wd;
     const float *rowf;     // set by the launcher: factors inside Wd
-    const uint32_t *mask;  // selection, or nullptr: every channel
+    const float *inv;      // set by the launcher: per-token scale and the staged kept values
+    const void *xh;
+    const uint32_t *mask;  // selection
     const float *eta;      // token shift, or nullptr
     const float *rowsum;
     void *y;
     int out_bf16;
     int stream_all;        // read every channel's codes whatever the mask
-    int after_select;      // the previous kernel in the stream is this call's selection
 };
-cudaError_t launch_decode_fp4(DecodeFp4Args a, int fmt, cudaStream_t st);
+// Workspace offsets: keep words at 0, eta, scale factors, staged x.
+struct DecodeFp4Layout {
+    size_t eta, inv, xh, bytes;
+};
+DecodeFp4Layout decode_fp4_layout(int T, int K);
+// `selected`: sel.bitmask and sel.eta hold the selection already; otherwise
+// the staging kernel makes it (N:M, threshold, keep-all) and writes them.
+cudaError_t launch_decode_fp4(DecodeFp4Args a, const SelectArgs &sel, bool selected, void *ws, int fmt,
+                              cudaStream_t st);
 
 // Norm / residual step (norm.cu).
 struct NormArgs {
