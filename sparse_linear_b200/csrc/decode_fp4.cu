@@ -134,15 +134,16 @@ cudaError_t launch_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const
 // (the same code and order as k_select_nm_decode: identical bits) for the mean
 // and the largest |x|, selects its own channels (or takes a mask) and writes
 // the keep words and the kept values as f16 parts, in the order the decode
-// reads them: [16-channel step][part][token of TP][16].  Rows of tokens past T
-// are not written: they only reach output columns past T.
+// reads them: [16-channel step][column][16], part p of token t in column
+// p * pstride + t.  Columns of no token are not written: they only reach sums
+// that are not read.
 constexpr int DS_THREADS = 256;
 constexpr int DS_CHUNK = DS_THREADS * 8;
 constexpr int DS_ROWREG = 8;  // row loads in flight per thread
 
 struct StageArgs {
     const void *x;
-    int T, K, TP;
+    int T, K, cols, pstride;
     int score_f, sel, n, m, dpts;  // score_f: multiply |x| by f
     float tau;
     const float *eta_static, *f;
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(DS_THREADS) k_fp4_stage(StageArgs a)
     const float mul = pow2f(e);
 #pragma unroll
     for (int k = 0; k < 8; ++k) xh[k] = (keep >> k) & 1u ? __fmul_rn(xh[k], mul) : 0.0f;
-    __half *out = a.xh + ((size_t)(c0 >> 4) * PARTS * a.TP + t) * 16 + (c0 & 8);
+    __half *out = a.xh + ((size_t)(c0 >> 4) * a.cols + t) * 16 + (c0 & 8);
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
         uint32_t w[4];
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(DS_THREADS) k_fp4_stage(StageArgs a)
                 xh[2 * k + 1] = isinf(h1) ? 0.0f : xh[2 * k + 1] - h1;
             }
         }
-        *reinterpret_cast<uint4 *>(out + (size_t)p * a.TP * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(out + (size_t)p * a.pstride * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -264,25 +265,32 @@ __global__ void __launch_bounds__(DS_THREADS) k_fp4_stage(StageArgs a)
 // CTA (rank of a cluster, slice): the slice's 128 columns and a contiguous
 // part of K; its warps take 16-channel steps in turn, each with a cp.async
 // ring of its own (codes of kept rows, scales, staged x of a step).  Rows that
-// no token keeps are not loaded: their kept values are zero and a code is
-// finite whatever its bits.  The warps' sums are added in shared memory and
-// the cluster's through distributed shared memory, both in a fixed order.
+// no token keeps are not loaded (but for the first steps, which are asked for
+// before the selection is known): their kept values are zero and a code is
+// finite whatever its bits.  The warps' sums are added in shared memory; each
+// CTA then sends every other its share of them and adds up what it receives,
+// both in a fixed order.
+//
+// NT: 8-column tiles of staged values.  A value of two parts takes two columns
+// of one tile while both fit (up to 4 tokens in one tile, up to 8 in two);
+// PARTS = 2 (9 to 16 tokens) runs the second part as MMAs of its own.
 template <int NT, int PARTS>
 struct DfCfg {
     static constexpr int TP = 8 * NT;
     static constexpr int XB = PARTS * TP * 32;       // staged x of a step, bytes
     static constexpr int STAGE = DF_CODES + XB;
-    static constexpr int DEPTH = NT * PARTS == 4 ? 6 : 8;  // steps in flight per warp: two CTAs per SM fit
+    static constexpr int DEPTH = NT * PARTS == 4 ? 5 : (NT == 2 ? 7 : 8);  // steps in flight per warp: two CTAs per SM fit
     static constexpr size_t ring = (size_t)DF_WARPS * DEPTH * STAGE;
     static constexpr size_t red = (size_t)DF_WARPS * TP * DF_RSTRIDE * 4;
-    static constexpr size_t smem = ring > red ? ring : red;
+    static constexpr size_t big = ring > red ? ring : red;
+    static constexpr size_t recv = (size_t)TP * DF_COLS * 4 + 16 * 8 * 4;  // the shares of 8 CTAs, rounded up
+    static constexpr size_t smem = big + recv;
+    static_assert(smem + 4 * 1024 + 1024 <= 113 * 1024, "two CTAs per SM");
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // Four bytes of two codes each -> four f16x2.
@@ -333,7 +341,7 @@ __device__ __forceinline__ void df_scales(uint32_t sc, float (&f)[4])
     }
 }
 
-constexpr int DF_MAXW = 1024;  // keep words of a CTA's range held in shared memory
+constexpr int DF_MAXW = 512;  // keep words of a CTA's range held in shared memory
 
 template <int NT, int PARTS, int FMT>
 __global__ void __launch_bounds__(DF_THREADS, 2) k_decode_fp4(DecodeFp4Args a)
@@ -355,60 +363,62 @@ __global__ void __launch_bounds__(DF_THREADS, 2) k_decode_fp4(DecodeFp4Args a)
     // step s of this warp: channels 32 w0 + 16 (DF_WARPS s + warp) ..
     const int nsteps = 2 * (w1 - w0);
     const int mine = nsteps > warp ? (nsteps - warp + DF_WARPS - 1) / DF_WARPS : 0;
-    const uint8_t *xsrc = reinterpret_cast<const uint8_t *>(a.xh) + (size_t)(2 * w0) * C::XB;
     // 16-byte piece `lane` (and lane + 32) of the 16 rows: row 4r + q of channel 4q + r
     const int bit0 = 4 * ((lane >> 2) & 3) + (lane >> 4), bit1 = bit0 + 2;
+    // sources of the step that is issued next, and its slot
+    const int b0 = 2 * w0 + warp;
+    constexpr size_t CSTEP = (size_t)DF_WARPS * (FMT == AS_FP4_NV ? df_unit(FMT) : df_unit(FMT) / 2);
+    const uint8_t *cp = (FMT == AS_FP4_NV ? wslice + (size_t)b0 * df_unit(FMT)
+                                          : wslice + (size_t)(b0 >> 1) * df_unit(FMT) + (b0 & 1) * 1024) + 16 * lane;
+    const size_t sc_off = FMT == AS_FP4_NV ? 1024 : 2048 - (b0 & 1) * 1024;  // scales from the step's codes
+    const uint8_t *xp = reinterpret_cast<const uint8_t *>(a.xh) + (size_t)b0 * C::XB + 16 * lane;
 
-    auto issue_codes = [&](int s, uint32_t keep) {
-        const int b = 2 * w0 + DF_WARPS * s + warp;
-        const uint8_t *unit = FMT == AS_FP4_NV ? wslice + (size_t)b * df_unit(FMT)
-                                               : wslice + (size_t)(b >> 1) * df_unit(FMT) + (b & 1) * 1024;
-        const uint8_t *sc = FMT == AS_FP4_NV ? unit + 1024 : wslice + (size_t)(b >> 1) * df_unit(FMT) + 2048;
-        const uint32_t dst = ring + (uint32_t)(s % DEPTH) * C::STAGE + 16 * lane;
-        if ((keep >> bit0) & 1u) cp_async16(dst, unit + 16 * lane, 16u);
-        if ((keep >> bit1) & 1u) cp_async16(dst + 512, unit + 512 + 16 * lane, 16u);
-        if (lane < 8) cp_async16(dst + 1024, sc + 16 * lane, 16u);
+    auto issue_codes = [&](uint32_t dst, uint32_t keep) {
+        if ((keep >> bit0) & 1u) cp_async16(dst, cp, 16u);
+        if ((keep >> bit1) & 1u) cp_async16(dst + 512, cp + 512, 16u);
+        if (lane < 8) cp_async16(dst + 1024, cp + sc_off, 16u);
+        cp += CSTEP;
     };
-    auto issue_x = [&](int s) {
-        const uint8_t *src = xsrc + (size_t)(DF_WARPS * s + warp) * C::XB + 16 * lane;
-        const uint32_t dst = ring + (uint32_t)(s % DEPTH) * C::STAGE + DF_CODES + 16 * lane;
+    auto issue_x = [&](uint32_t dst) {
 #pragma unroll
         for (int i = 0; i < (C::XB + 511) / 512; ++i)
-            if (512 * i + 16 * lane < C::XB) cp_async16(dst + 512 * i, src + 512 * i, 16u);
+            if (512 * i + 16 * lane < C::XB) cp_async16(dst + DF_CODES + 512 * i, xp + 512 * i, 16u);
+        xp += (size_t)DF_WARPS * C::XB;
     };
-    auto kept_rows = [&](int s) -> uint32_t {
-        if (a.stream_all) return 0xFFFFu;
-        const int lb = DF_WARPS * s + warp, w = lb >> 1;
-        uint32_t u = w < DF_MAXW ? s_union[w] : 0xFFFFFFFFu;
-        return (u >> (16 * (lb & 1))) & 0xFFFFu;
-    };
+    const uint32_t my = ring + 16 * lane;
 
+    // Remote stores need their CTA to be running: the wait for these arrivals
+    // comes before the first of them.
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
     // The staging kernel lets this one start after its own wait, so everything
-    // before that kernel in the stream (the weights among it) is complete: if
-    // every channel is wanted, the codes of the first steps come before the
-    // wait for the staged x.
-    if (a.stream_all)
-        for (int s = 0; s < DEPTH - 1; ++s)
-            if (s < mine) issue_codes(s, 0xFFFFu);
+    // before that kernel in the stream (the weights among it) is complete: the
+    // codes of the first steps come before the wait for the staged x, whole,
+    // since the selection is not known yet.
+#pragma unroll
+    for (int s = 0; s < DEPTH - 1; ++s)
+        if (s < mine) issue_codes(my + s * C::STAGE, 0xFFFFu);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!a.stream_all) {
+#pragma unroll
+    for (int s = 0; s < DEPTH - 1; ++s) {
+        if (s < mine) issue_x(my + s * C::STAGE);
+        cp_async_commit();  // the first group also holds the codes before the wait
+    }
+    // rows that some token keeps, for the steps that are still to be issued
+    if (!a.stream_all && nsteps > DF_WARPS * (DEPTH - 1)) {
         for (int w = tid; w < min(w1 - w0, DF_MAXW); w += DF_THREADS) {
             uint32_t u = 0;
-#pragma unroll
-            for (int t = 0; t < TP; ++t)
-                if (t < T && as_in((long long)t * nwords + w0 + w, (long long)T * nwords))
+            for (int t = 0; t < T; ++t)
+                if (as_in((long long)t * nwords + w0 + w, (long long)T * nwords))
                     u |= a.mask[(size_t)t * nwords + w0 + w];
             s_union[w] = u;
         }
         __syncthreads();
     }
-    for (int s = 0; s < DEPTH - 1; ++s) {
-        if (s < mine) {
-            if (!a.stream_all) issue_codes(s, kept_rows(s));
-            issue_x(s);
-        }
-        cp_async_commit();  // with stream_all the first group also holds the codes before the wait
-    }
+    auto kept_rows = [&](int s) -> uint32_t {
+        const int lb = DF_WARPS * s + warp, w = lb >> 1;
+        if (a.stream_all || w >= DF_MAXW) return 0xFFFFu;
+        return (s_union[w] >> (16 * (lb & 1))) & 0xFFFFu;
+    };
 
     float acc[8][NT][4];
 #pragma unroll
@@ -418,10 +428,10 @@ __global__ void __launch_bounds__(DF_THREADS, 2) k_decode_fp4(DecodeFp4Args a)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
 
+    uint32_t src = ring, dst = my + (DEPTH - 1) * C::STAGE;
     for (int s = 0; s < mine; ++s) {
         cp_async_wait<DEPTH - 2>();
         __syncwarp();  // a step's pieces were copied by all lanes
-        const uint32_t src = ring + (uint32_t)(s % DEPTH) * C::STAGE;
         uint32_t wv[4][2];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -438,10 +448,13 @@ __global__ void __launch_bounds__(DF_THREADS, 2) k_decode_fp4(DecodeFp4Args a)
                 asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(bx[n][p][0]), "=r"(bx[n][p][1])
                              : "r"(src + DF_CODES + (p * TP + 8 * n + g8) * 32 + q4 * 8) : "memory");
         if (s + DEPTH - 1 < mine) {  // into the slot read at s - 1
-            issue_codes(s + DEPTH - 1, kept_rows(s + DEPTH - 1));
-            issue_x(s + DEPTH - 1);
+            issue_codes(dst, kept_rows(s + DEPTH - 1));
+            issue_x(dst);
         }
         cp_async_commit();
+        dst = src + 16 * lane;  // free after this step
+        src += C::STAGE;
+        if (src == ring + DEPTH * C::STAGE) src = ring;
 #pragma unroll
         for (int wd = 0; wd < 2; ++wd) {
             // codes of a channel pair in one byte: outputs p = 8 wd + 2 b (A[0],
@@ -487,26 +500,35 @@ __global__ void __launch_bounds__(DF_THREADS, 2) k_decode_fp4(DecodeFp4Args a)
             r0[DF_RSTRIDE + 8] = acc[m][n][3];
         }
     __syncthreads();
-    for (int i = tid; i < T * DF_COLS; i += DF_THREADS) {
+    // element i of the T * 128 sums belongs to CTA i / share; rank r's share of
+    // it lands in slot r of that CTA
+    const int total = T * DF_COLS, share = (total + nranks - 1) / nranks;
+    float *recv = reinterpret_cast<float *>(smem + C::big);
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster has started
+    for (int i = tid; i < total; i += DF_THREADS) {
         const int t = i / DF_COLS, at = t * DF_RSTRIDE + i % DF_COLS;
-        float s = red[at];
+        float s = 0.0f;
 #pragma unroll
-        for (int w = 1; w < DF_WARPS; ++w) s += red[w * TP * DF_RSTRIDE + at];
-        red[at] = s * a.inv[t];
+        for (int w = 0; w < DF_WARPS; ++w) {
+            s += red[w * TP * DF_RSTRIDE + at];
+            if (a.part_cols) s += red[w * TP * DF_RSTRIDE + at + a.part_cols * DF_RSTRIDE];  // the second part
+        }
+        const int owner = i / share;
+        st_cluster_f32(mapa_u32(smem_u32(recv + rank * share + i - owner * share), (uint32_t)owner), s * a.inv[t]);
     }
     cluster_sync_all();
-    for (int i = rank * DF_THREADS + tid; i < T * DF_COLS; i += nranks * DF_THREADS) {
+    for (int k = tid; k < share; k += DF_THREADS) {
+        const int i = rank * share + k;
+        if (i >= total) break;
         const int t = i / DF_COLS, o = slice * DF_COLS + i % DF_COLS;
-        const uint32_t at = smem_u32(red + t * DF_RSTRIDE + i % DF_COLS);
-        float s = 0.0f;
-        for (int r = 0; r < nranks; ++r) s += ld_cluster_f32(mapa_u32(at, (uint32_t)r));
         if (o >= n_out || !as_in((long long)t * n_out + o, (long long)T * n_out)) continue;
+        float s = 0.0f;
+        for (int r = 0; r < nranks; ++r) s += recv[r * share + k];
         s *= a.rowf[o];
         if (a.eta) s = fmaf(a.eta[t], a.rowsum[o], s);
         if (a.out_bf16) static_cast<__nv_bfloat16 *>(a.y)[(size_t)t * n_out + o] = __float2bfloat16_rn(s);
         else static_cast<float *>(a.y)[(size_t)t * n_out + o] = s;
     }
-    cluster_sync_all();  // no CTA leaves while another reads its sums
 }
 
 // CTAs of a cluster (along K): as many as fill the GPU (two per SM), at least
@@ -539,31 +561,39 @@ static void df_launch(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 g
 }
 
 template <int NT, int PARTS, int FMT>
-static cudaError_t launch_df(const DecodeFp4Args &a, const StageArgs &sa, cudaStream_t st)
+static cudaError_t launch_df(const DecodeFp4Args &a, cudaStream_t st)
 {
     using C = DfCfg<NT, PARTS>;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    df_launch(cfg, attr, dim3(a.T, (a.K + DS_CHUNK - 1) / DS_CHUNK), DS_THREADS, 0, 0, st);
-    cudaError_t e = a.bf16 ? cudaLaunchKernelEx(&cfg, k_fp4_stage<__nv_bfloat16, PARTS>, sa)
-                           : cudaLaunchKernelEx(&cfg, k_fp4_stage<float, PARTS>, sa);
-    if (e != cudaSuccess) return e;
     static int done[64];
-    e = smem_limit_once(k_decode_fp4<NT, PARTS, FMT>, C::smem, done);
+    cudaError_t e = smem_limit_once(k_decode_fp4<NT, PARTS, FMT>, C::smem, done);
     if (e != cudaSuccess) return e;
     const int ranks = df_ranks(a.K, a.n_out);
     df_launch(cfg, attr, dim3(ranks, (a.n_out + DF_COLS - 1) / DF_COLS), DF_THREADS, C::smem, ranks, st);
     return cudaLaunchKernelEx(&cfg, k_decode_fp4<NT, PARTS, FMT>, a);
 }
 
-template <int NT, int FMT>
-static cudaError_t launch_df_parts(const DecodeFp4Args &a, const StageArgs &sa, cudaStream_t st)
+template <int PARTS>
+static cudaError_t launch_stage(const StageArgs &s, int bf16, cudaStream_t st)
 {
-    // a bf16 value without a shift fits one f16 part
-    return a.bf16 && !a.eta ? launch_df<NT, 1, FMT>(a, sa, st) : launch_df<NT, 2, FMT>(a, sa, st);
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    df_launch(cfg, attr, dim3(s.T, (s.K + DS_CHUNK - 1) / DS_CHUNK), DS_THREADS, 0, 0, st);
+    return bf16 ? cudaLaunchKernelEx(&cfg, k_fp4_stage<__nv_bfloat16, PARTS>, s)
+                : cudaLaunchKernelEx(&cfg, k_fp4_stage<float, PARTS>, s);
 }
 
-static int df_tpad(int T) { return T <= 8 ? 8 : 16; }
+// columns that staged values take: parts of a token side by side while they
+// fit two tiles
+static int df_cols(int T, int parts) { return T * parts <= 8 ? 8 : (T * parts <= 16 ? 16 : 32); }
+
+template <int FMT>
+static cudaError_t launch_df_cols(const DecodeFp4Args &a, int cols, cudaStream_t st)
+{
+    if (cols == 8) return launch_df<1, 1, FMT>(a, st);
+    return cols == 16 ? launch_df<2, 1, FMT>(a, st) : launch_df<2, 2, FMT>(a, st);
+}
 
 // keep words, eta, scale factors, staged x (for two parts)
 DecodeFp4Layout decode_fp4_layout(int T, int K)
@@ -573,7 +603,7 @@ DecodeFp4Layout decode_fp4_layout(int T, int K)
     l.eta = up((size_t)T * ((K + 31) / 32) * sizeof(uint32_t));
     l.inv = l.eta + up((size_t)T * sizeof(float));
     l.xh = l.inv + up((size_t)T * sizeof(float));
-    l.bytes = l.xh + up((size_t)K * df_tpad(T) * 2 * sizeof(__half));
+    l.bytes = l.xh + up((size_t)K * df_cols(T, 2) * sizeof(__half));
     return l;
 }
 
@@ -588,7 +618,11 @@ cudaError_t launch_decode_fp4(DecodeFp4Args a, const SelectArgs &sel, bool selec
     s.x = a.x;
     s.T = a.T;
     s.K = a.K;
-    s.TP = df_tpad(a.T);
+    // a bf16 value without a shift fits one f16 part
+    const int parts = a.bf16 && !a.eta ? 1 : 2;
+    s.cols = df_cols(a.T, parts);
+    s.pstride = s.cols / 2;
+    a.part_cols = parts == 2 && s.cols <= 16 ? s.pstride : 0;
     s.score_f = sel.f != nullptr;
     s.sel = sel.sel;
     s.n = sel.n;
@@ -603,9 +637,9 @@ cudaError_t launch_decode_fp4(DecodeFp4Args a, const SelectArgs &sel, bool selec
     s.eta = sel.eta;
     s.inv = reinterpret_cast<float *>(w + l.inv);
     s.xh = reinterpret_cast<__half *>(w + l.xh);
-    if (fmt == AS_FP4_NV)
-        return a.T <= 8 ? launch_df_parts<1, AS_FP4_NV>(a, s, st) : launch_df_parts<2, AS_FP4_NV>(a, s, st);
-    return a.T <= 8 ? launch_df_parts<1, AS_FP4_MX>(a, s, st) : launch_df_parts<2, AS_FP4_MX>(a, s, st);
+    const cudaError_t e = parts == 1 ? launch_stage<1>(s, a.bf16, st) : launch_stage<2>(s, a.bf16, st);
+    if (e != cudaSuccess) return e;
+    return fmt == AS_FP4_NV ? launch_df_cols<AS_FP4_NV>(a, s.cols, st) : launch_df_cols<AS_FP4_MX>(a, s.cols, st);
 }
 
 }  // namespace as

@@ -201,6 +201,7 @@ struct DecodeFp4Args {
     void *y;
     int out_bf16;
     int stream_all;        // read every channel's codes whatever the mask
+    int part_cols;         // columns from a value's first to its second part; 0: none, or MMAs of its own
 };
 // Workspace offsets: keep words at 0, eta, scale factors, staged x.
 struct DecodeFp4Layout {
