@@ -574,12 +574,11 @@ as_status as_linear_prefill_fp4(const uint8_t *xq, const uint8_t *x_sf, const fl
                                 const uint8_t *Wq, const uint8_t *w_sf, const float *w_scale, as_fp4 fmt,
                                 as_dtype out_dtype, void *y, cudaStream_t stream);
 
-/* Decode weights, once per layer: the quantised weight [n_out, K] re-laid so
- * that a kept channel's codes are contiguous for 128 output columns.  Wd is
- * opaque, as_fp4_decode_bytes(n_out, K, fmt) bytes, and carries w_scale
- * (NULL: 1).  An output whose row holds a NaN scale gives NaN; AS_FP4_MX
- * blocks whose scale is below 2^-126 times their row's largest count as zero.
- * as_fp4_decode_bytes is host-only and 0 if the arguments are invalid. */
+/* Decode weights, once per layer: the quantised weight [n_out, K] re-laid in
+ * tiles of 128 outputs x 256 channels, codes and scales as the tensor cores
+ * take them.  Wd is opaque, as_fp4_decode_bytes(n_out, K, fmt) bytes, and
+ * carries w_scale (NULL: 1).  as_fp4_decode_bytes is host-only and 0 if the
+ * arguments are invalid. */
 size_t as_fp4_decode_bytes(int n_out, int K, as_fp4 fmt);
 as_status as_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const float *w_scale, int n_out, int K,
                              as_fp4 fmt, uint8_t *Wd, cudaStream_t stream);
@@ -587,12 +586,14 @@ as_status as_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const float
 /* as_linear_decode on 4-bit weights: 1 <= T <= 16 tokens,
  *   y = prune(x) W^T (+ eta_t rowsum_o with a token shift),
  * W the values that Wq stands for.  Scores, selection, shift and the outputs
- * mask_out, eta_out, colnorm_out are those of as_linear_decode; x is not
- * quantised: each token is scaled by a power of two and its kept values enter
- * the tensor cores with 22 bits (all 8 of an unshifted bf16 value), values
- * below 2^-28 of the token's largest with an error of 2^-39 of it.  g and rowsum
- * describe the same W (as_weight_prep on its values).  Only the codes of
- * channels that some token keeps are read.
+ * mask_out, eta_out, colnorm_out are those of as_linear_decode.  x is not
+ * rounded to 4 bits: a kept value enters the tensor cores as a sum of 4-bit
+ * parts with scales of their own, 10 (AS_FP4_NV) or 11 (AS_FP4_MX) for float32
+ * output and 7 or 8 for bf16 output, which leave less than 2^-25 or 2^-17 of
+ * the largest kept value of its block of 16 or 32 channels (AS_FP4_NV: or, in
+ * a block that is smaller than 2^-14 of its token's largest value, of that).  g and rowsum
+ * describe the same W (as_weight_prep on its values).  A non-finite kept value
+ * or weight scale makes the outputs that read it NaN.
  *   x [T, K] in `dt`; K % 32 == 0, n_out % 8 == 0; cfg->var is not supported.
  *   Workspace: as_workspace_size(AS_OP_DECODE_FP4, T, K, n_out, cfg); no
  *   zero-fill needed, left in an unspecified state. */

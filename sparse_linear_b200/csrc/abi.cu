@@ -57,7 +57,7 @@ size_t decode_ws(int T, int K, int n_out, const as_config *cfg, int bf16)
 
 size_t decode_fp4_ws(int T, int K, const as_config *cfg)
 {
-    return decode_fp4_layout(T, K).bytes +
+    return decode_fp4_layout(T, K, cfg->out_dtype == AS_BF16).bytes +
            (cfg->score == AS_SCORE_CLACT ? round_up(colnorm_workspace(T, K), 256) : 0);
 }
 
@@ -680,7 +680,7 @@ extern "C" as_status as_linear_decode_fp4(const void *x, as_dtype dt, int T, int
     if (!aligned16(workspace)) return AS_ERR_ALIGN;
     if (!workspace || ws_bytes < decode_fp4_ws(T, K, cfg)) return AS_ERR_WORKSPACE;
     const int bf16 = dt == AS_BF16;
-    const DecodeFp4Layout lay = decode_fp4_layout(T, K);
+    const DecodeFp4Layout lay = decode_fp4_layout(T, K, cfg->out_dtype == AS_BF16);
     char *ws = static_cast<char *>(workspace);
 
     SelectArgs s{};
@@ -715,19 +715,10 @@ extern "C" as_status as_linear_decode_fp4(const void *x, as_dtype dt, int T, int
     a.K = K;
     a.n_out = n_out;
     a.Wd = Wd;
-    a.mask = s.bitmask;
     a.eta = s.eta;
     a.rowsum = rowsum;
     a.y = y;
     a.out_bf16 = cfg->out_dtype == AS_BF16;
-    DecodeArgs d{};  // the expected share of channels that some token keeps
-    d.T = T;
-    d.K = K;
-    d.sel = cfg->sel;
-    d.n = cfg->n;
-    d.m = cfg->m;
-    d.k_keep = cfg->k_keep;
-    a.stream_all = decode_streams_all(d);
     return cuda_status(launch_decode_fp4(a, s, topk, workspace, fmt, stream));
 }
 

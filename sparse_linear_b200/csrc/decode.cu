@@ -1054,8 +1054,7 @@ static double expected_union(const DecodeArgs &a)
 }
 
 // DENSE streaming when the union is expected to reach 97 % of the channels.
-bool decode_streams_all(const DecodeArgs &a) { return expected_union(a) >= 0.97; }
-static bool decode_dense(const DecodeArgs &a, int tpad) { return !decode_fused(tpad, a.sel, a.K) && decode_streams_all(a); }
+static bool decode_dense(const DecodeArgs &a, int tpad) { return !decode_fused(tpad, a.sel, a.K) && expected_union(a) >= 0.97; }
 
 template <int TP, bool FUSED, bool LO, bool DENSE>
 static cudaError_t launch_tc_one(const DecodeArgs &a, const DecodePlan &p, cudaStream_t st)

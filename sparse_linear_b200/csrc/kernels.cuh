@@ -79,8 +79,6 @@ bool decode_needs_select(int T, int K, int n_out, int bf16, int out_bf16, int se
 int decode_launch_count(const DecodeArgs &a, const DecodePlan &p);
 // True when a bf16 decode of this token pad and selection is one fused launch.
 bool decode_fused(int tpad, int sel, int K);
-// Whether nearly every channel is expected to be kept by some token.
-bool decode_streams_all(const DecodeArgs &a);
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &p, cudaStream_t st);
 
 // ------------------------------------------------------------ prefill GEMM
@@ -192,22 +190,21 @@ struct DecodeFp4Args {
     int bf16;
     int T, K, n_out;
     const uint8_t *Wd;
-    const float *rowf;     // set by the launcher: factors inside Wd
-    const float *inv;      // set by the launcher: per-token scale and the staged kept values
-    const void *xh;
-    const uint32_t *mask;  // selection
     const float *eta;      // token shift, or nullptr
     const float *rowsum;
     void *y;
     int out_bf16;
-    int stream_all;        // read every channel's codes whatever the mask
-    int part_cols;         // columns from a value's first to its second part; 0: none, or MMAs of its own
+    // set by the launcher: parts per value, columns (T * P rounded up), factors
+    // inside Wd, column scales and images in the workspace
+    int P, N;
+    const float *rowf, *scale;
+    const uint8_t *xq;
 };
-// Workspace offsets: keep words at 0, eta, scale factors, staged x.
+// Workspace offsets: keep words at 0, eta, column scales, staged columns.
 struct DecodeFp4Layout {
-    size_t eta, inv, xh, bytes;
+    size_t eta, scale, xq, bytes;
 };
-DecodeFp4Layout decode_fp4_layout(int T, int K);
+DecodeFp4Layout decode_fp4_layout(int T, int K, int out_bf16);
 // `selected`: sel.bitmask and sel.eta hold the selection already; otherwise
 // the staging kernel makes it (N:M, threshold, keep-all) and writes them.
 cudaError_t launch_decode_fp4(DecodeFp4Args a, const SelectArgs &sel, bool selected, void *ws, int fmt,

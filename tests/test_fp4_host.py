@@ -112,8 +112,8 @@ def test_sizes(lib):
     assert lib.as_fp4_sf_bytes(1, 32, lib.AS_FP4_NV) == 512
     assert lib.as_fp4_sf_bytes(129, 4096, lib.AS_FP4_NV) == 2 * 64 * 512
     assert lib.as_fp4_sf_bytes(128, 4096 + 32, lib.AS_FP4_MX) == 33 * 512
-    assert lib.as_fp4_decode_bytes(136, 64, lib.AS_FP4_NV) == 2 * 4 * 1152 + 2 * 128 * 8
-    assert lib.as_fp4_decode_bytes(128, 64, lib.AS_FP4_MX) == 2 * 2176 + 128 * 8
+    assert lib.as_fp4_decode_bytes(136, 544, lib.AS_FP4_NV) == 2 * 3 * (16384 + 2048) + 2 * 128 * 4
+    assert lib.as_fp4_decode_bytes(128, 64, lib.AS_FP4_MX) == 16384 + 1024 + 128 * 4
     for rows, K, fmt in ((0, 64, 0), (1, 48, 1), (1, 0, 1), (1, 131072 + 32, 1), (1, 64, 2)):
         with pytest.raises(lib.ASError):
             lib.as_fp4_sf_bytes(rows, K, fmt)
