@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank(), nranks = gridDim.x, mt = blockIdx.y;
     const int nkb = (a.K + DF_KB - 1) / DF_KB, per = (nkb + nranks - 1) / nranks;
     const int kb0 = min(nkb, rank * per), kb1 = min(nkb, kb0 + per);
@@ -385,41 +385,40 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_fp4<FMT>(128, a.N);
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ready = false;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!ready && !mbar_wait(&full[stage], phase)) { *(volatile int *)abort_flag = 1; break; }
-                tc_fence_after();
-                const int next = stage + 1 == S ? 0 : stage + 1;
-                const uint32_t nphase = stage + 1 == S ? phase ^ 1 : phase;
-                ready = kb + 1 < kb1 && mbar_try_wait(&full[next], nphase);
-                const int steps = min(4, (a.K - kb * DF_KB + 63) >> 6);
-                const uint32_t sfa = tmem + NB + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
-                const uint32_t xsf = smem_u32(sX + stage * P::XB + NB * 128);
+        const uint32_t lead = elect_lane();
+        const uint32_t idesc = idesc_fp4<FMT>(128, a.N);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ready = false;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!ready && !mbar_wait(&full[stage], phase)) { *(volatile int *)abort_flag = 1; break; }
+            tc_fence_after();
+            const int next = stage + 1 == S ? 0 : stage + 1;
+            const uint32_t nphase = stage + 1 == S ? phase ^ 1 : phase;
+            ready = kb + 1 < kb1 && mbar_try_wait(&full[next], nphase);
+            const int steps = min(4, (a.K - kb * DF_KB + 63) >> 6);
+            const uint32_t sfa = tmem + NB + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
+            const uint32_t xsf = smem_u32(sX + stage * P::XB + NB * 128);
 #pragma unroll
-                for (int t = 0; t < C::SFT; ++t) {
-                    tmem_cp_sf<false>(sfa + 4 * t, sdesc_rows16(smem_u32(sSA + stage * P::SA + 512 * t)));
+            for (int t = 0; t < C::SFT; ++t) {
+                tmem_cp_sf(lead, sfa + 4 * t, sdesc_rows16(smem_u32(sSA + stage * P::SA + 512 * t)));
 #pragma unroll
-                    for (int c = 0; c < P::NSB; ++c)
-                        tmem_cp_sf<false>(sfb + 4 * P::NSB * t + 4 * c, sdesc_rows16(xsf + c * C::SFB + 512 * t));
-                }
-                const uint64_t a_desc = sdesc_kmajor_sw128(smem_u32(sW + stage * P::W));
-                const uint64_t b_desc = sdesc_kmajor_sw128(smem_u32(sX + stage * P::XB));
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < steps)
-                        mma_fp4<FMT, false>(tmem, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4),
-                                            idesc | C::ids(j), sfa + 4 * C::tile(j), sfb + 4 * P::NSB * C::tile(j),
-                                            (kb > kb0 || j > 0));
-                tc_commit(&empty[stage]);
-                stage = next;
-                phase = nphase;
+                for (int c = 0; c < P::NSB; ++c)
+                    tmem_cp_sf(lead, sfb + 4 * P::NSB * t + 4 * c, sdesc_rows16(xsf + c * C::SFB + 512 * t));
             }
-            tc_commit(done);  // every MMA above has completed
+            const uint64_t a_desc = sdesc_kmajor_sw128(smem_u32(sW + stage * P::W));
+            const uint64_t b_desc = sdesc_kmajor_sw128(smem_u32(sX + stage * P::XB));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < steps)
+                    mma_fp4<FMT, false>(lead, tmem, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4),
+                                        idesc | C::ids(j), sfa + 4 * C::tile(j), sfb + 4 * P::NSB * C::tile(j),
+                                        (kb > kb0 || j > 0));
+            tc_commit_lead<false>(lead, &empty[stage]);
+            stage = next;
+            phase = nphase;
         }
+        tc_commit_lead<false>(lead, done);  // every MMA above has completed
     }
     __syncwarp();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster has started

@@ -30,46 +30,65 @@
 
 namespace as {
 
-// D[tmem] (+)= (A * scales) (B * scales)^T; PAIR: over a CTA pair.
-template <int FMT, bool PAIR>
-__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate)
+// The issuing warp runs its loop as a whole and every tcgen05 instruction is
+// predicated on one elected lane (`lead`): addresses and descriptors then stay
+// in uniform registers.  Issued from a branch of one lane each instruction cost
+// some 90 clocks of moves.
+__device__ __forceinline__ uint32_t elect_lane()
 {
-    if constexpr (PAIR && FMT == AS_FP4_NV)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-    else if constexpr (PAIR)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-    else if constexpr (FMT == AS_FP4_NV)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
+    uint32_t lead;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(lead));
+    return lead;
 }
 
+// Index of this warp, known to be the same in all its lanes.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+
+// D[tmem] (+)= (A * scales) (B * scales)^T; PAIR: over a CTA pair.
+#define AS_MMA_FP4(GROUP, VEC)                                                                                    \
+    asm volatile(                                                                                                 \
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"                            \
+        "@q tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC                            \
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa),     \
+        "r"(sfb), "r"(accumulate), "r"(lead)                                                                       \
+        : "memory")
+template <int FMT, bool PAIR>
+__device__ __forceinline__ void mma_fp4(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate)
+{
+    if constexpr (PAIR && FMT == AS_FP4_NV) AS_MMA_FP4("2", "4X");
+    else if constexpr (PAIR) AS_MMA_FP4("2", "2X");
+    else if constexpr (FMT == AS_FP4_NV) AS_MMA_FP4("1", "4X");
+    else AS_MMA_FP4("1", "2X");
+}
+#undef AS_MMA_FP4
+
 // 512 bytes (32 rows x 16 bytes) of shared memory -> 4 TMEM columns, repeated
-// in the four lane quarters; PAIR: in each CTA of the pair from its own.
+// in the four lane quarters.
+__device__ __forceinline__ void tmem_cp_sf(uint32_t lead, uint32_t taddr, uint64_t s_desc)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                 "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(s_desc), "r"(lead)
+                 : "memory");
+}
+
+// Arrive on `bar` (PAIR: in both CTAs) once this lane's tcgen05 operations so
+// far have completed.
 template <bool PAIR>
-__device__ __forceinline__ void tmem_cp_sf(uint32_t taddr, uint64_t s_desc)
+__device__ __forceinline__ void tc_commit_lead(uint32_t lead, uint64_t *bar)
 {
     if constexpr (PAIR)
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+            "%1;\n\t}" ::"r"(smem_u32(bar)), "h"((uint16_t)3), "r"(lead)
+            : "memory");
     else
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                     "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                         smem_u32(bar)),
+                     "r"(lead)
+                     : "memory");
 }
 
 // Instruction descriptor of kind::mxf4nvf4: A and B format code 1 (E2M1) in
@@ -163,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
     __shared__ __align__(16) float s_ws[8][128];  // every epilogue warp's weight row scales
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int num_tiles = p.m_tiles * p.n_tiles;
@@ -218,7 +237,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader only)
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
+            const uint32_t lead = elect_lane();
             constexpr uint32_t idesc = idesc_fp4<FMT>(PAIR_BM, PAIR_BN);
             int stage = 0;
             uint32_t phase = 0;
@@ -242,17 +262,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (j < steps)
-                            mma_fp4<FMT, true>(tmem, a_desc + (uint64_t)((32 * j) >> 4),
+                            mma_fp4<FMT, true>(lead, tmem, a_desc + (uint64_t)((32 * j) >> 4),
                                                b_desc + (uint64_t)((32 * j) >> 4), idesc | C::ids(j),
                                                sfa + 4 * C::tile(j), sfb + 8 * C::tile(j), (kb | j) != 0);
-                    tc_commit_pair_mc(&empty[stage], 0x3);  // frees the stage and its scales in both CTAs
+                    tc_commit_lead<true>(lead, &empty[stage]);  // frees the stage and its scales in both CTAs
                     stage = next;
                     phase = nphase;
                 }
                 if (!ok) { *(volatile int *)abort_flag = 1; break; }
-                tc_commit_pair_mc(acc_full, 0x3);
+                tc_commit_lead<true>(lead, acc_full);
             }
-            tc_commit_pair(drain);
+            tc_commit_lead<true>(lead, drain);
             mbar_wait(drain, 0);
         }
     } else if (warp == 14) {
@@ -441,7 +461,7 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 1);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank(), nranks = gridDim.x;
     const int ot = blockIdx.y, tt = blockIdx.z;  // output tile, token tile
     const int per = (p.k_blocks + nranks - 1) / nranks;
@@ -488,36 +508,40 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_fp4<FMT>(128, N);
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(&full[stage], phase)) { *(volatile int *)abort_flag = 1; break; }
-                tc_fence_after();
-                const int steps = min(4, (p.K - kb * C::KB + 63) >> 6);
-                const uint32_t sfa = tmem + N + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
+        const uint32_t lead = elect_lane();
+        constexpr uint32_t idesc = idesc_fp4<FMT>(128, N);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ready = false;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!ready && !mbar_wait(&full[stage], phase)) { *(volatile int *)abort_flag = 1; break; }
+            tc_fence_after();
+            const int next = stage + 1 == S ? 0 : stage + 1;
+            const uint32_t nphase = stage + 1 == S ? phase ^ 1 : phase;
+            ready = kb + 1 < kb1 && mbar_try_wait(&full[next], nphase);
+            const int steps = min(4, (p.K - kb * C::KB + 63) >> 6);
+            const uint32_t sfa = tmem + N + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
 #pragma unroll
-                for (int t = 0; t < C::SFT; ++t) {
-                    tmem_cp_sf<false>(sfa + 4 * t, sdesc_rows16(smem_u32(sSA + stage * P::SA + 512 * t)));
+            for (int t = 0; t < C::SFT; ++t) {
+                tmem_cp_sf(lead, sfa + 4 * t, sdesc_rows16(smem_u32(sSA + stage * P::SA + 512 * t)));
 #pragma unroll
-                    for (int c = 0; c < P::NSB; ++c)
-                        tmem_cp_sf<false>(sfb + 4 * P::NSB * t + 4 * c,
-                                          sdesc_rows16(smem_u32(sSB + stage * P::SB + c * C::SFB + 512 * t)));
-                }
-                const uint64_t a_desc = sdesc_kmajor_sw128(smem_u32(sA + stage * P::A));
-                const uint64_t b_desc = sdesc_kmajor_sw128(smem_u32(sB + stage * P::B));
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < steps)
-                        mma_fp4<FMT, false>(tmem, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4),
-                                            idesc | C::ids(j), sfa + 4 * C::tile(j),
-                                            sfb + 4 * P::NSB * C::tile(j), (kb > kb0 || j > 0));
-                tc_commit(&empty[stage]);
-                if (++stage == S) { stage = 0; phase ^= 1; }
+                for (int c = 0; c < P::NSB; ++c)
+                    tmem_cp_sf(lead, sfb + 4 * P::NSB * t + 4 * c,
+                               sdesc_rows16(smem_u32(sSB + stage * P::SB + c * C::SFB + 512 * t)));
             }
-            tc_commit(done);  // every MMA above has completed
+            const uint64_t a_desc = sdesc_kmajor_sw128(smem_u32(sA + stage * P::A));
+            const uint64_t b_desc = sdesc_kmajor_sw128(smem_u32(sB + stage * P::B));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < steps)
+                    mma_fp4<FMT, false>(lead, tmem, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4),
+                                        idesc | C::ids(j), sfa + 4 * C::tile(j), sfb + 4 * P::NSB * C::tile(j),
+                                        (kb > kb0 || j > 0));
+            tc_commit_lead<false>(lead, &empty[stage]);
+            stage = next;
+            phase = nphase;
         }
+        tc_commit_lead<false>(lead, done);  // every MMA above has completed
     }
     // ---- all MMAs done: the accumulator (row = output, column = token) goes
     // to shared memory transposed, over the drained ring
