@@ -243,44 +243,50 @@ __global__ void __launch_bounds__(DS_THREADS) k_fp4_stage(StageArgs a)
     const int off = (c0 & 255) >> 1;                          // byte of the row
     constexpr int LANES = fp4_block(FMT) / 8;                 // lanes of a block
     const int blk = (c0 & 255) / fp4_block(FMT);              // block of the K block
+#pragma unroll 2
     for (int p = 0; p < a.P; ++p) {
         uint32_t am = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) am = max(am, __float_as_uint(xh[k]) & 0x7FFFFFFFu);
 #pragma unroll
         for (int o = 1; o < LANES; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-        Fp4Block b;
-        float back;  // value of a code of 1
+        // Any scale and any of two codes next to a border will do here, the rest
+        // follows them: no exact divisions.  Infinities and NaN take the NaN
+        // scale, and with it the outputs.
+        const bool bad = am >= F32_INF_BITS;
+        uint32_t byte;
+        float back, fwd;  // value of a code of 1 and its inverse, 0 where the scale is 0
         if constexpr (FMT == AS_FP4_NV) {
             const int e = max(e0 - 2 * p, -126);
-            b = fp4_block_scale<FMT>(am, pow2f(-e));
-            back = b.s * pow2f(e);
+            byte = bad ? 127u : (uint32_t)__nv_cvt_float_to_fp8(__uint_as_float(am) * pow2f(-e) * (1.0f / 6.0f),
+                                                                __NV_SATFINITE, __NV_E4M3);
+            const float sv = bad ? 0.0f : e4m3_value(byte);
+            back = sv * pow2f(e);
+            fwd = sv > 0.0f ? __fdividef(1.0f, sv) * pow2f(-e) : 0.0f;
         } else {
             // the smallest power of two that leaves no value above 6: one more
             // than the quantiser's where the mantissa is above 1.5
-            b = fp4_block_scale<FMT>(am, 1.0f);
-            if (b.byte < 254u && (am & 0x7FFFFFu) > 0x400000u && am >= 0x01800000u) {
-                ++b.byte;
-                b.pre *= 0.5f;
-            }
-            back = fp4_scale_value<FMT>(b.byte);
+            const int f = (int)(am >> 23) - 2 + ((am & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+            byte = bad ? 255u : (uint32_t)min(max(f, 1), 253);  // normal powers of two
+            back = bad ? 0.0f : __uint_as_float(byte << 23);
+            fwd = bad ? 0.0f : __uint_as_float((254u - byte) << 23);
         }
-        // any of two codes next to a border will do here: the rest follows it
-        const uint32_t codes = fp4_codes8<FMT, true>(xh, b, FMT == AS_FP4_NV ? __frcp_rn(b.s > 0.0f ? b.s : 1.0f) : 1.0f);
+        uint32_t codes = 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) codes |= e2m1x2(xh[2 * k] * fwd, xh[2 * k + 1] * fwd) << (8 * k);
+        if (bad) codes = 0u;
         if (write) {
             const int row = t * a.P + a.P - 1 - p;
             *reinterpret_cast<uint32_t *>(img + row * 128 + ((((off >> 4) ^ (row & 7)) << 4) | (off & 15))) = codes;
             if ((lane & (LANES - 1)) == 0)
                 img[(size_t)a.N * 128 + (row >> 7) * C::SFB + (blk >> 2) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
-                    (blk & 3)] = (uint8_t)b.byte;
+                    (blk & 3)] = (uint8_t)byte;
         }
-        if (b.s > 0.0f) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // the rest, exact: code * scale has at most 7 bits
-                const float2 q = e2m1x2_value((codes >> (8 * k)) & 0xFFu);
-                xh[2 * k] = fmaf(-q.x, back, xh[2 * k]);
-                xh[2 * k + 1] = fmaf(-q.y, back, xh[2 * k + 1]);
-            }
+        for (int k = 0; k < 4; ++k) {  // the rest, exact: code * scale has at most 7 bits
+            const float2 q = e2m1x2_value((codes >> (8 * k)) & 0xFFu);
+            xh[2 * k] = fmaf(-q.x, back, xh[2 * k]);
+            xh[2 * k + 1] = fmaf(-q.y, back, xh[2 * k + 1]);
         }
     }
 }
@@ -318,6 +324,7 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
     constexpr int S = P::STAGES;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(16) float recv[DF_RECV];
+    __shared__ float s_scale[NB], s_rowf[DF_ROWS], s_rowsum[DF_ROWS], s_eta[16];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                             ~uintptr_t(1023));
     unsigned char *sW = smem, *sX = sW + S * P::W, *sSA = sX + S * P::XB;  // every W and X image 1024-byte aligned
@@ -426,7 +433,14 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
     auto first_of = [&](int r) { return (r * 128 + nranks - 1) / nranks; };
     const int width = (127 + nranks) / nranks;  // room per CTA and token
     if (warp >= 2) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // the columns' scales
+        // factors, while the MMAs run
+        const int u = (int)threadIdx.x - 64, uo = mt * DF_ROWS + u;
+        s_rowf[u] = a.rowf[uo];
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the staging kernel's columns and means
+        s_rowsum[u] = a.eta && uo < a.n_out ? a.rowsum[uo] : 0.0f;
+        for (int i = u; i < a.T * a.P; i += 128) s_scale[i] = a.scale[i];
+        if (u < a.T) s_eta[u] = a.eta ? a.eta[u] : 0.0f;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
         const bool ok = mbar_wait(done, 0);
         tc_fence_after();
         const int q = warp & 3, o = 32 * q + lane;
@@ -453,7 +467,7 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 if (c + i < a.T * a.P) {
-                    v = fmaf(__uint_as_float(r[i]), a.scale[c + i], v);
+                    v = fmaf(__uint_as_float(r[i]), s_scale[c + i], v);
                     if (++p == a.P) {
                         st_cluster_f32(to + 4u * (uint32_t)(t * width), v);
                         v = 0.0f;
@@ -464,8 +478,6 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
             }
         }
         tc_fence_before();
-    } else {
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // eta
     }
     __syncwarp();
     cluster_sync_all();
@@ -476,8 +488,8 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
         if (o >= a.n_out || !as_in((long long)t * a.n_out + o, (long long)a.T * a.n_out)) continue;
         float s = 0.0f;
         for (int r = 0; r < nranks; ++r) s += recv[(r * a.T + t) * width + c];
-        s *= a.rowf[o];
-        if (a.eta) s = fmaf(a.eta[t], a.rowsum[o], s);
+        s *= s_rowf[o0 + c];
+        if (a.eta) s = fmaf(s_eta[t], s_rowsum[o0 + c], s);
         if (a.out_bf16) static_cast<__nv_bfloat16 *>(a.y)[(size_t)t * a.n_out + o] = __float2bfloat16_rn(s);
         else static_cast<float *>(a.y)[(size_t)t * a.n_out + o] = s;
     }
