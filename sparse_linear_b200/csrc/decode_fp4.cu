@@ -23,7 +23,10 @@
 //
 // Kernels of a call, chained by programmatic dependent launch: (top-k: the
 // selection kernel,) k_fp4_stage, which makes the selection and the parts,
-// and k_decode_fp4, whose weight copies start before the parts are ready.
+// and k_decode_fp4, whose weight copies start before the parts are ready.  (One
+// kernel, every CTA making the parts of its own channels, took 15.0 us against
+// 10.7 us for one token at 11008 x 4096: the row's mean and the parts are then
+// computed 32 times over, beside the weight stream.)
 #include "common.cuh"
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -122,22 +125,24 @@ cudaError_t launch_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const
 }
 
 // ------------------------------------------------------------------ staging
-// Grid (token, 2048-channel chunk).  Every CTA of a token reads the whole row
-// (the same code and order as k_select_nm_decode: identical bits) for the mean
-// and the largest |x|, selects its own channels (or takes a mask), writes the
-// keep words and turns the kept values into P parts.  Part p of token t is
-// column t P + P - 1 - p (the small parts first).  The columns of a K block are the operand image that the
-// decode copies in one piece: N rows of 128 bytes (128-byte swizzle), then the
-// scale tiles of 128 rows.  Rows past T P are not written: they only reach
-// sums that are not read.
+// A cluster per token, its CTAs and their warps share the row's 256-channel
+// tiles: mean and largest |x| are exchanged through distributed shared memory,
+// then every warp selects its own channels (or takes a mask), writes the keep
+// words and turns the kept values into P parts.  Part p of token t is
+// column t P + P - 1 - p (the small parts first).  The columns of a K block are
+// the operand image that the decode copies in one piece: N rows of 128 bytes
+// (128-byte swizzle), then the scale tiles of 128 rows.  Rows past T P are not
+// written: they only reach sums that are not read.
 //   The row scale of part p is S_0 4^-p (NV; S_0 from the largest |x - eta|):
 // a part's rest is at most its scale, 448 S_p = 6 * 448 * S_p / 6 <= 2688 S_p/4.
-constexpr int DS_THREADS = 256;
-constexpr int DS_CHUNK = DS_THREADS * 8;
-constexpr int DS_ROWREG = 8;  // row loads in flight per thread
+// The mean is a float64 sum in a fixed order (of bf16 values it is exact, so
+// its order does not show).
+// Bound: latency (the parts are a chain of some 150 clocks each).
+constexpr int DS_WARPS = 8;
 
 struct StageArgs {
     const void *x;
+    int bf16;
     int T, K, P, N;
     int score_f, sel, n, m, dpts;  // score_f: multiply |x| by f
     float tau;
@@ -151,82 +156,46 @@ struct StageArgs {
     size_t xb;
 };
 
-template <typename TX, int FMT>
-__global__ void __launch_bounds__(DS_THREADS) k_fp4_stage(StageArgs a)
+// 8 values of token t from channel c0 on.
+__device__ __forceinline__ void df_load8(const StageArgs &a, int t, int c0, float (&v)[8])
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // after the wait: see k_select_nm_decode
-    using C = Fp4Cfg<FMT>;
-    __shared__ double red[DS_THREADS / 32];
-    __shared__ uint32_t redm[DS_THREADS / 32];
-    const int t = blockIdx.x, chunk = blockIdx.y;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int K = a.K, ng = K >> 3, words = (K + 31) >> 5;
-    const TX *xr = static_cast<const TX *>(a.x) + (size_t)t * K;
-    const int c0 = chunk * DS_CHUNK + warp * 256 + 8 * lane;  // this lane's 8 channels
-    const bool act = c0 < K;
+    const size_t at = (size_t)t * a.K + c0;
+    if (a.bf16) load8(static_cast<const __nv_bfloat16 *>(a.x) + at, v);
+    else load8(static_cast<const float *>(a.x) + at, v);
+}
 
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, f[8];
-    if (act) load8(xr + c0, v);
+// Exponent of S_0: |x - eta| is at most top + |eta|.
+template <int FMT>
+__device__ __forceinline__ int df_exponent(uint32_t top, float eta)
+{
+    if (FMT == AS_FP4_MX) return 0;
+    return nv_row_exponent(min(__float_as_uint(__uint_as_float(top) + fabsf(eta)), F32_INF_BITS - 1u));
+}
+// Row scale of part p.
+template <int FMT>
+__device__ __forceinline__ float df_part_scale(int e0, int p)
+{
+    return FMT == AS_FP4_NV ? pow2f(max(e0 - 2 * p, -126)) : 1.0f;
+}
+
+// Kept values of this lane's 8 channels (a warp: 256 channels from a multiple
+// of 256 on; act: below K), selected here unless mask_in.
+__device__ __forceinline__ void df_keep8(const StageArgs &a, int t, int c0, bool act, float eta, float (&xh)[8])
+{
+    const int lane = threadIdx.x & 31, words = (a.K + 31) >> 5;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, f[8], sc[8];
+    if (act) df_load8(a, t, c0, v);
     const bool has_f = a.score_f && act && !a.mask_in;
     if (has_f) load8f(a.f + c0, f);
-    uint32_t word = 0xFFFFFFFFu;
-    if (a.mask_in && act) word = a.mask_in[(size_t)t * words + (c0 >> 5)];
-    float eta = !a.dpts ? 0.0f : (a.mask_in ? a.eta_in[t] : (a.dpts == AS_PTS_STATIC ? a.eta_static[t] : 0.0f));
-    const bool mean = a.dpts == AS_PTS_DYNAMIC && !a.mask_in;
-
-    double sum = 0.0;
-    uint32_t top = 0;  // largest finite |x| (bits)
-    for (int g0 = 0; g0 < ng; g0 += DS_ROWREG * DS_THREADS) {
-        float w[DS_ROWREG][8];
-#pragma unroll
-        for (int r = 0; r < DS_ROWREG; ++r) {
-            const int g = g0 + tid + r * DS_THREADS;
-            if (g < ng) load8(xr + 8 * (size_t)g, w[r]);
-        }
-#pragma unroll
-        for (int r = 0; r < DS_ROWREG; ++r) {
-            const int g = g0 + tid + r * DS_THREADS;
-            if (g < ng) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (mean) sum += (double)w[r][e];
-                    const uint32_t b = __float_as_uint(w[r][e]) & 0x7FFFFFFFu;
-                    top = max(top, b < F32_INF_BITS ? b : 0u);
-                }
-            }
-        }
-    }
-    if (mean) {
-        sum = warp_sum_f64(sum);
-        if (lane == 0) red[warp] = sum;
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) redm[warp] = top;
-    __syncthreads();
-    if (mean) {
-        double tot = 0.0;
-#pragma unroll
-        for (int w = 0; w < DS_THREADS / 32; ++w) tot += red[w];
-        eta = (float)(tot / (double)K);
-    }
-#pragma unroll
-    for (int w = 0; w < DS_THREADS / 32; ++w) top = max(top, redm[w]);
-    // |x - eta| is at most this (finite: the sum of two finite values may not be)
-    const uint32_t bound = min(__float_as_uint(__uint_as_float(top) + fabsf(eta)), F32_INF_BITS - 1u);
-    int e0 = FMT == AS_FP4_NV ? nv_row_exponent(bound) : 0;
-    if (chunk == 0 && tid < a.P) a.scale[t * a.P + a.P - 1 - tid] = FMT == AS_FP4_NV ? pow2f(max(e0 - 2 * tid, -126)) : 1.0f;
-    if (chunk == 0 && tid == 0 && a.dpts && !a.mask_in) a.eta[t] = eta;
-    float xh[8], sc[8];
     score8(v, a.dpts, eta, has_f ? f : nullptr, 0, xh, sc);
     uint32_t keep;
     if (a.mask_in) {
-        keep = (word >> (8 * (lane & 3))) & 0xFFu;
+        keep = act ? (a.mask_in[(size_t)t * words + (c0 >> 5)] >> (8 * (lane & 3))) & 0xFFu : 0u;
     } else {
         keep = a.sel == AS_SEL_NM ? nm_keep_dispatch(sc, lane, a.n, a.m)
                                   : (a.sel == AS_SEL_THRESH ? keep_thresh(sc, a.tau) : 0xFFu);
         if (!act) keep = 0;
-        word = keep << (8 * (lane & 3));
+        uint32_t word = keep << (8 * (lane & 3));
         word |= __shfl_xor_sync(0xffffffffu, word, 1);
         word |= __shfl_xor_sync(0xffffffffu, word, 2);
         const int wi = c0 >> 5;
@@ -235,59 +204,156 @@ __global__ void __launch_bounds__(DS_THREADS) k_fp4_stage(StageArgs a)
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) xh[k] = act && ((keep >> k) & 1u) ? xh[k] : 0.0f;
+}
 
-    // parts; channels up to the next multiple of 64 are written (zeros): an
-    // instruction covers 64
-    const bool write = c0 < (K + 63) / 64 * 64;
-    uint8_t *img = a.xq + (size_t)(c0 >> 8) * a.xb;
+// The P parts of 8 kept values into their K block's image `img` (rows of 128
+// bytes, scale tiles at sf).  Channels up to the next multiple of 64 past K are
+// written (zeros): an instruction covers 64.
+template <int FMT>
+__device__ __forceinline__ void df_parts8(const StageArgs &a, int t, int c0, int e0, float (&xh)[8], uint8_t *img,
+                                          uint8_t *sf)
+{
+    using C = Fp4Cfg<FMT>;
+    const int lane = threadIdx.x & 31;
+    const bool write = c0 < (a.K + 63) / 64 * 64;
     const int off = (c0 & 255) >> 1;                          // byte of the row
     constexpr int LANES = fp4_block(FMT) / 8;                 // lanes of a block
     const int blk = (c0 & 255) / fp4_block(FMT);              // block of the K block
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(xh[k]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // a block that holds an infinity or a NaN takes the NaN scale, and with it
+    // the outputs
+    const bool bad = top >= F32_INF_BITS;
+    const int row0 = t * a.P;
+    uint8_t *sfb = sf + (blk >> 2) * 512 + (blk & 3);
+    const bool sf_lane = write && (lane & (LANES - 1)) == 0;
 #pragma unroll 2
     for (int p = 0; p < a.P; ++p) {
-        uint32_t am = 0;
+        float am = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) am = max(am, __float_as_uint(xh[k]) & 0x7FFFFFFFu);
+        for (int k = 0; k < 8; ++k) am = fmaxf(am, fabsf(xh[k]));
 #pragma unroll
-        for (int o = 1; o < LANES; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+        for (int o = 1; o < LANES; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
         // Any scale and any of two codes next to a border will do here, the rest
-        // follows them: no exact divisions.  Infinities and NaN take the NaN
-        // scale, and with it the outputs.
-        const bool bad = am >= F32_INF_BITS;
-        uint32_t byte;
-        float back, fwd;  // value of a code of 1 and its inverse, 0 where the scale is 0
+        // follows them: no exact divisions.
+        int byte;
+        uint32_t sbits;  // the whole scale
         if constexpr (FMT == AS_FP4_NV) {
-            const int e = max(e0 - 2 * p, -126);
-            byte = bad ? 127u : (uint32_t)__nv_cvt_float_to_fp8(__uint_as_float(am) * pow2f(-e) * (1.0f / 6.0f),
-                                                                __NV_SATFINITE, __NV_E4M3);
-            const float sv = bad ? 0.0f : e4m3_value(byte);
-            back = sv * pow2f(e);
-            fwd = sv > 0.0f ? __fdividef(1.0f, sv) * pow2f(-e) : 0.0f;
+            // am / 6 rounded to 4 significant bits; below E4M3's normal numbers
+            // the block waits for a part with a smaller row scale
+            sbits = (__float_as_uint(am * (1.0f / 6.0f)) + 0x80000u) & 0xFFF00000u;
+            byte = (int)(sbits >> 20) - 8 * (max(e0 - 2 * p, -126) + 120);
+            if (byte < 8) byte = 0, sbits = 0u;
+            if (byte > 126) byte = 126, sbits = (uint32_t)(126 + 8 * (max(e0 - 2 * p, -126) + 120)) << 20;
+            if (bad) byte = 127;
         } else {
             // the smallest power of two that leaves no value above 6: one more
             // than the quantiser's where the mantissa is above 1.5
-            const int f = (int)(am >> 23) - 2 + ((am & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-            byte = bad ? 255u : (uint32_t)min(max(f, 1), 253);  // normal powers of two
-            back = bad ? 0.0f : __uint_as_float(byte << 23);
-            fwd = bad ? 0.0f : __uint_as_float((254u - byte) << 23);
+            const uint32_t m = __float_as_uint(am);
+            byte = min(max((int)(m >> 23) - 2 + ((m & 0x7FFFFFu) > 0x400000u ? 1 : 0), 1), 253);  // normal powers of two
+            sbits = (uint32_t)byte << 23;
+            if (bad) byte = 255;
         }
+        const float back = __uint_as_float(sbits);
+        const float fwd = sbits ? __fdividef(1.0f, back) : 0.0f;
         uint32_t codes = 0u;
 #pragma unroll
         for (int k = 0; k < 4; ++k) codes |= e2m1x2(xh[2 * k] * fwd, xh[2 * k + 1] * fwd) << (8 * k);
         if (bad) codes = 0u;
-        if (write) {
-            const int row = t * a.P + a.P - 1 - p;
+        const int row = row0 + a.P - 1 - p;
+        if (write)
             *reinterpret_cast<uint32_t *>(img + row * 128 + ((((off >> 4) ^ (row & 7)) << 4) | (off & 15))) = codes;
-            if ((lane & (LANES - 1)) == 0)
-                img[(size_t)a.N * 128 + (row >> 7) * C::SFB + (blk >> 2) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
-                    (blk & 3)] = (uint8_t)byte;
-        }
+        if (sf_lane) sfb[(row >> 7) * C::SFB + (row & 31) * 16 + ((row >> 5) & 3) * 4] = (uint8_t)byte;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // the rest, exact: code * scale has at most 7 bits
             const float2 q = e2m1x2_value((codes >> (8 * k)) & 0xFFu);
             xh[2 * k] = fmaf(-q.x, back, xh[2 * k]);
             xh[2 * k + 1] = fmaf(-q.y, back, xh[2 * k + 1]);
         }
+    }
+}
+
+__device__ __forceinline__ float df_given_eta(const StageArgs &a, int t)
+{
+    return !a.dpts ? 0.0f : (a.mask_in ? a.eta_in[t] : (a.dpts == AS_PTS_STATIC ? a.eta_static[t] : 0.0f));
+}
+
+__device__ __forceinline__ void st_cluster_b64(uint32_t addr, uint64_t v)
+{
+    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(DS_WARPS * 32) k_fp4_stage(StageArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // after the wait: see k_select_nm_decode
+    __shared__ double w_sum[DS_WARPS];
+    __shared__ uint32_t w_max[DS_WARPS];
+    __shared__ __align__(8) uint64_t c_sum[8], c_max[8];  // of every CTA
+    const int t = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int rank = (int)cluster_ctarank(), ranks = gridDim.x;
+    const int nkb = (a.K + 255) >> 8, per = (nkb + ranks - 1) / ranks;
+    const int kb0 = min(nkb, rank * per), kb1 = min(nkb, kb0 + per);
+    float eta = df_given_eta(a, t);
+    uint32_t top = 0;
+    const bool mean = a.dpts == AS_PTS_DYNAMIC && !a.mask_in;
+    if (mean || FMT == AS_FP4_NV) {  // uniform over the cluster
+        double sum = 0.0;
+        for (int kb = kb0 + warp; kb < kb1; kb += warps) {
+            const int c0 = 256 * kb + 8 * lane;
+            if (c0 < a.K) {
+                float v[8];
+                df_load8(a, t, c0, v);
+                if (mean)
+                    sum += (((double)v[0] + (double)v[1]) + ((double)v[2] + (double)v[3])) +
+                           (((double)v[4] + (double)v[5]) + ((double)v[6] + (double)v[7]));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t b = __float_as_uint(v[e]) & 0x7FFFFFFFu;
+                    top = max(top, b < F32_INF_BITS ? b : 0u);
+                }
+            }
+        }
+        if (mean) sum = warp_sum_f64(sum);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) {
+            w_sum[warp] = sum;
+            w_max[warp] = top;
+        }
+        asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // this CTA runs
+        __syncthreads();
+        sum = 0.0;
+        for (int w = 0; w < warps; ++w) {
+            sum += w_sum[w];
+            top = max(top, w_max[w]);
+        }
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if ((int)threadIdx.x < ranks) {
+            st_cluster_b64(mapa_u32(smem_u32(&c_sum[rank]), threadIdx.x), (uint64_t)__double_as_longlong(sum));
+            st_cluster_b64(mapa_u32(smem_u32(&c_max[rank]), threadIdx.x), (uint64_t)top);
+        }
+        cluster_sync_all();
+        sum = 0.0;
+        for (int r = 0; r < ranks; ++r) {
+            sum += __longlong_as_double((long long)c_sum[r]);
+            top = max(top, (uint32_t)c_max[r]);
+        }
+        if (mean) eta = (float)(sum / (double)a.K);
+    }
+    const int e0 = df_exponent<FMT>(top, eta);
+    if (rank == 0 && (int)threadIdx.x < a.P)
+        a.scale[t * a.P + a.P - 1 - threadIdx.x] = df_part_scale<FMT>(e0, threadIdx.x);
+    if (rank == 0 && threadIdx.x == 0 && a.dpts && !a.mask_in) a.eta[t] = eta;
+    for (int kb = kb0 + warp; kb < kb1; kb += warps) {
+        const int c0 = 256 * kb + 8 * lane;
+        float xh[8];
+        df_keep8(a, t, c0, c0 < a.K, eta, xh);
+        uint8_t *img = a.xq + (size_t)kb * a.xb;
+        df_parts8<FMT>(a, t, c0, e0, xh, img, img + (size_t)a.N * 128);
     }
 }
 
@@ -303,10 +369,10 @@ struct DfCfg {
     static constexpr int NSB = (NB + 127) / 128;
     static constexpr int W = DF_WTILE, SA = Fp4Cfg<FMT>::SFB;
     static constexpr int XB = NB * 128 + NSB * Fp4Cfg<FMT>::SFB;
-    static constexpr int STAGE = W + SA + XB;
     static constexpr int SCOLS = 4 * (1 + NSB) * Fp4Cfg<FMT>::SFT;
     static constexpr int STAGES = NB <= 32 ? 8 : (NB <= 64 ? 7 : (NB <= 128 ? 5 : 4));
-    static constexpr size_t smem = 1024 + (size_t)STAGES * STAGE + 256;
+    static constexpr size_t smem = 1024 + (size_t)STAGES * (W + SA + XB) + 256;
+    static_assert(smem + 12 * 1024 <= 227 * 1024, "shared memory");
     static_assert(NB + STAGES * SCOLS <= 512, "tensor memory");
 };
 constexpr int DF_RECV = 16 * (128 + 8);  // floats: T outputs' shares from up to 8 CTAs
@@ -314,6 +380,32 @@ constexpr int DF_RECV = 16 * (128 + 8);  // floats: T outputs' shares from up to
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// A token's P columns times their scales, for every token, to the owner of
+// this lane's output.  (P is a constant so that the columns stay in registers.)
+template <int P>
+__device__ __forceinline__ void df_send(uint32_t acc, bool some, int T, int width, const float *scale, uint32_t to)
+{
+    for (int t = 0; t < T; ++t) {
+        uint32_t r[16];  // columns past P belong to others and are not used
+        if (some) {
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                  "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                : "r"(acc + (uint32_t)(t * P)));
+            tmem_ld_wait();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = 0u;
+        }
+        float v = 0.0f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) v = fmaf(__uint_as_float(r[p]), scale[t * P + p], v);
+        st_cluster_f32(to + 4u * (uint32_t)(t * width), v);
+    }
 }
 
 template <int FMT, int NB>
@@ -327,8 +419,9 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
     __shared__ float s_scale[NB], s_rowf[DF_ROWS], s_rowsum[DF_ROWS], s_eta[16];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                             ~uintptr_t(1023));
-    unsigned char *sW = smem, *sX = sW + S * P::W, *sSA = sX + S * P::XB;  // every W and X image 1024-byte aligned
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S * P::STAGE);
+    // every W and X image is 1024-byte aligned
+    unsigned char *sW = smem, *sX = sW + S * P::W, *sSA = sX + S * P::XB;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sSA + S * P::SA);
     uint64_t *full = bars, *empty = bars + S, *done = bars + 2 * S;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 1);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
@@ -359,7 +452,6 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
     // remote stores need their CTA to be running: the wait for these arrivals
     // comes before the first of them
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-
     if (warp == 0) {
         if (lane == 0) {
             const uint8_t *w = a.Wd + (size_t)mt * nkb * df_unit(FMT);
@@ -375,8 +467,8 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
                 bulk_load(sX + s * P::XB, src, (uint32_t)a.N * 128, &full[s]);
                 bulk_load(sX + s * P::XB + NB * 128, src + (size_t)a.N * 128, P::NSB * C::SFB, &full[s]);
             };
-            // The staging kernel lets this one start after its own wait, so
-            // everything before it in the stream, the weights among it, is
+            // The kernel before this one in its call lets it start after its
+            // own wait, so everything before that, the weights among it, is
             // complete: only x waits for it.
             const int first = min(S, kb1 - kb0);
             for (int i = 0; i < first; ++i) load_w(kb0 + i, i);
@@ -405,7 +497,8 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
             ready = kb + 1 < kb1 && mbar_try_wait(&full[next], nphase);
             const int steps = min(4, (a.K - kb * DF_KB + 63) >> 6);
             const uint32_t sfa = tmem + NB + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
-            const uint32_t xsf = smem_u32(sX + stage * P::XB + NB * 128);
+            const unsigned char *x = sX + stage * P::XB;
+            const uint32_t xsf = smem_u32(x + NB * 128);
 #pragma unroll
             for (int t = 0; t < C::SFT; ++t) {
                 tmem_cp_sf(lead, sfa + 4 * t, sdesc_rows16(smem_u32(sSA + stage * P::SA + 512 * t)));
@@ -414,7 +507,7 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
                     tmem_cp_sf(lead, sfb + 4 * P::NSB * t + 4 * c, sdesc_rows16(xsf + c * C::SFB + 512 * t));
             }
             const uint64_t a_desc = sdesc_kmajor_sw128(smem_u32(sW + stage * P::W));
-            const uint64_t b_desc = sdesc_kmajor_sw128(smem_u32(sX + stage * P::XB));
+            const uint64_t b_desc = sdesc_kmajor_sw128(smem_u32(x));
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j < steps)
@@ -436,8 +529,8 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
         // factors, while the MMAs run
         const int u = (int)threadIdx.x - 64, uo = mt * DF_ROWS + u;
         s_rowf[u] = a.rowf[uo];
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // the staging kernel's columns and means
         s_rowsum[u] = a.eta && uo < a.n_out ? a.rowsum[uo] : 0.0f;
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the staging kernel's columns and means
         for (int i = u; i < a.T * a.P; i += 128) s_scale[i] = a.scale[i];
         if (u < a.T) s_eta[u] = a.eta ? a.eta[u] : 0.0f;
         asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -446,36 +539,14 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
         const int q = warp & 3, o = 32 * q + lane;
         const int owner = o * nranks >> 7;
         const uint32_t to = mapa_u32(smem_u32(recv + (size_t)rank * a.T * width + o - first_of(owner)), (uint32_t)owner);
+        const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
         const bool some = ok && kb1 > kb0;
-        int t = 0, p = 0;
-        float v = 0.0f;
-        for (int c = 0; c < a.T * a.P; c += 16) {
-            uint32_t r[16];
-            if (some) {
-                asm volatile(
-                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                    "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                    : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                      "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                      "=r"(r[15])
-                    : "r"(tmem + ((uint32_t)(32 * q) << 16) + c));
-                tmem_ld_wait();
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) r[i] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (c + i < a.T * a.P) {
-                    v = fmaf(__uint_as_float(r[i]), s_scale[c + i], v);
-                    if (++p == a.P) {
-                        st_cluster_f32(to + 4u * (uint32_t)(t * width), v);
-                        v = 0.0f;
-                        p = 0;
-                        ++t;
-                    }
-                }
-            }
+        if (FMT == AS_FP4_NV) {
+            if (a.P == 7) df_send<7>(acc, some, a.T, width, s_scale, to);
+            else df_send<10>(acc, some, a.T, width, s_scale, to);
+        } else {
+            if (a.P == 8) df_send<8>(acc, some, a.T, width, s_scale, to);
+            else df_send<11>(acc, some, a.T, width, s_scale, to);
         }
         tc_fence_before();
     }
@@ -515,6 +586,13 @@ static void df_launch(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 g
     cfg.numAttrs = ranks > 0 ? 2 : 1;
 }
 
+// CTAs of a cluster: as many as fill the GPU (one per SM), at most one per K
+// block and the portable cluster size.
+static int df_ranks(int K, int n_out)
+{
+    return std::max(1, std::min({sm_count() / df_mtiles(n_out), 8, df_kblocks(K)}));
+}
+
 template <int FMT, int NB>
 static cudaError_t launch_df(const DecodeFp4Args &a, cudaStream_t st)
 {
@@ -522,13 +600,10 @@ static cudaError_t launch_df(const DecodeFp4Args &a, cudaStream_t st)
     static int done[64];
     const cudaError_t e = smem_limit_once(k_decode_fp4<FMT, NB>, P::smem, done);
     if (e != cudaSuccess) return e;
-    // CTAs of a cluster: as many as fill the GPU (one per SM), at most one per
-    // K block and the portable cluster size
-    const int mtiles = df_mtiles(a.n_out);
-    const int ranks = std::max(1, std::min({sm_count() / mtiles, 8, df_kblocks(a.K)}));
+    const int ranks = df_ranks(a.K, a.n_out);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    df_launch(cfg, attr, dim3(ranks, mtiles), DF_THREADS, P::smem, ranks, st);
+    df_launch(cfg, attr, dim3(ranks, df_mtiles(a.n_out)), DF_THREADS, P::smem, ranks, st);
     return cudaLaunchKernelEx(&cfg, k_decode_fp4<FMT, NB>, a);
 }
 
@@ -537,9 +612,9 @@ static cudaError_t launch_df_fmt(const DecodeFp4Args &a, const StageArgs &s, cud
 {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    df_launch(cfg, attr, dim3(s.T, (s.K + DS_CHUNK - 1) / DS_CHUNK), DS_THREADS, 0, 0, st);
-    const cudaError_t e = a.bf16 ? cudaLaunchKernelEx(&cfg, k_fp4_stage<__nv_bfloat16, FMT>, s)
-                                 : cudaLaunchKernelEx(&cfg, k_fp4_stage<float, FMT>, s);
+    const int nkb = df_kblocks(s.K), ranks = std::min(8, nkb), warps = std::min(DS_WARPS, (nkb + ranks - 1) / ranks);
+    df_launch(cfg, attr, dim3(ranks, s.T), 32 * warps, 0, ranks, st);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_fp4_stage<FMT>, s);
     if (e != cudaSuccess) return e;
     if (a.N <= 16) return launch_df<FMT, 16>(a, st);
     if (a.N <= 32) return launch_df<FMT, 32>(a, st);
@@ -582,6 +657,7 @@ cudaError_t launch_decode_fp4(DecodeFp4Args a, const SelectArgs &sel, bool selec
     a.xq = reinterpret_cast<const uint8_t *>(w + l.xq);
     StageArgs s{};
     s.x = a.x;
+    s.bf16 = a.bf16;
     s.T = a.T;
     s.K = a.K;
     s.P = a.P;
