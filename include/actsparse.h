@@ -588,12 +588,11 @@ as_status as_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const float
  * W the values that Wq stands for.  Scores, selection, shift and the outputs
  * mask_out, eta_out, colnorm_out are those of as_linear_decode.  x is not
  * rounded to 4 bits: a kept value enters the tensor cores as a sum of 4-bit
- * parts with scales of their own, 10 (AS_FP4_NV) or 11 (AS_FP4_MX) for float32
- * output and 7 or 8 for bf16 output, which leave less than 2^-25 or 2^-17 of
- * the largest kept value of its block of 16 or 32 channels (AS_FP4_NV: or, in
- * a block that is smaller than 2^-14 of its token's largest value, of that).  g and rowsum
- * describe the same W (as_weight_prep on its values).  A non-finite kept value
- * or weight scale makes the outputs that read it NaN.
+ * parts, 10 for float32 output and 7 for bf16 output, which leave at most 2^-25
+ * or 2^-18 of the largest kept value of its block of 16 or 32 channels
+ * (AS_FP4_NV: or of 2^-17 of its token's largest, where that is more).  g and
+ * rowsum describe the same W (as_weight_prep on its values).  A non-finite
+ * kept value or weight scale makes the outputs that read it NaN.
  *   x [T, K] in `dt`; K % 32 == 0, n_out % 8 == 0; cfg->var is not supported.
  *   Workspace: as_workspace_size(AS_OP_DECODE_FP4, T, K, n_out, cfg); no
  *   zero-fill needed, left in an unspecified state. */

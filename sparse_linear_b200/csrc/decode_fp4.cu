@@ -3,18 +3,17 @@
 // The weights go to the tensor cores as they are stored, codes and block
 // scales (tcgen05.mma kind::mxf4nvf4), with the outputs on the M = 128 side,
 // so that nothing is unpacked and the kernel is bound by the bytes of W.  The
-// kept values of x enter as a sum of P four-bit parts: part p is the 4-bit
-// quantisation of what the parts before left over,
-//   xhat m = sum_p S_p s_pb code_p  (+ rest),
-// every subtraction exact in float32.  A part leaves at most 1/5.65 (NV: E4M3
-// scale, so that a block's largest value is 5.65 to 6.4 times its scale, and
-// half the largest step of E2M1 is 1) or 1/5 (MX: the largest value is 3 to 6
-// times the scale, and only a value of at least 5 can leave 1) of its block's
-// largest value.  float32 output takes 10 (NV) or 11 (MX) parts: the rest is
-// below 2^-25 of the block's largest; bf16 output takes 7 or 8: below 2^-17,
-// far inside the output's half step of 2^-9.  Each part of each token is a
-// column of the product (T P <= 176 of at most 256) and the epilogue adds a
-// token's columns in float32.
+// kept values of x enter as a sum of P four-bit parts,
+//   xhat m = sum_p S_p s_b code_p  (+ rest),  S_p = S_0 / 6^p,
+// with one scale s_b per block: the smallest E4M3 value (NV) or power of two
+// (MX) that leaves no value of the block above 6.  A code errs by at most half
+// the largest step of E2M1, 1, so that what a part leaves is at most 6 for the
+// next; P parts leave at most s_b S_0 / 6^P.  float32 output takes 10 parts,
+// which leave below 2^-25 of the block's largest value; bf16 output takes 7:
+// below 2^-18, far inside the output's half step of 2^-8.  S_p is a rounded
+// float32, which a value feels as one more rounding of 2^-24.  Each part of
+// each token is a column of the product (T P <= 160 of at most 256) and the
+// epilogue adds a token's columns in float32.
 //   Every channel's codes are read.  Reading only the rows of kept channels
 // was built first (channel-major codes, cp.async, unpacking for mma.sync):
 // 8:16 with one token halves the bytes, but the unpacking bound it: 14.5 us a
@@ -37,6 +36,7 @@ namespace as {
 constexpr int DF_ROWS = 128;  // outputs per tile
 constexpr int DF_KB = 256;    // channels per stage
 constexpr int DF_WTILE = DF_ROWS * DF_KB / 2;
+constexpr int DF_PARTS_BF16 = 7, DF_PARTS_F32 = 10;  // by the output's type
 
 static int df_kblocks(int K) { return (K + DF_KB - 1) / DF_KB; }
 static int df_mtiles(int n_out) { return (n_out + DF_ROWS - 1) / DF_ROWS; }
@@ -133,11 +133,9 @@ cudaError_t launch_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const
 // the operand image that the decode copies in one piece: N rows of 128 bytes
 // (128-byte swizzle), then the scale tiles of 128 rows.  Rows past T P are not
 // written: they only reach sums that are not read.
-//   The row scale of part p is S_0 4^-p (NV; S_0 from the largest |x - eta|):
-// a part's rest is at most its scale, 448 S_p = 6 * 448 * S_p / 6 <= 2688 S_p/4.
 // The mean is a float64 sum in a fixed order (of bf16 values it is exact, so
 // its order does not show).
-// Bound: latency (the parts are a chain of some 150 clocks each).
+// Bound: latency.
 constexpr int DS_WARPS = 8;
 
 struct StageArgs {
@@ -171,27 +169,41 @@ __device__ __forceinline__ int df_exponent(uint32_t top, float eta)
     if (FMT == AS_FP4_MX) return 0;
     return nv_row_exponent(min(__float_as_uint(__uint_as_float(top) + fabsf(eta)), F32_INF_BITS - 1u));
 }
-// Row scale of part p.
-template <int FMT>
-__device__ __forceinline__ float df_part_scale(int e0, int p)
+// Row scale of the next part; the same rounding wherever it is formed.
+__device__ __forceinline__ float df_next_scale(float S) { return __fmul_rn(S, 1.0f / 6.0f); }
+
+// What a lane needs of its 8 channels (a warp: 256 channels from a multiple of
+// 256 on; act: below K).
+struct DfRaw {
+    float v[8], f[8];
+    uint32_t word;  // keep word of mask_in
+};
+__device__ __forceinline__ void df_load_raw(const StageArgs &a, int t, int c0, bool act, DfRaw &r)
 {
-    return FMT == AS_FP4_NV ? pow2f(max(e0 - 2 * p, -126)) : 1.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = 0.0f, r.f[e] = 1.0f;
+    r.word = 0u;
+    if (!act) return;
+    df_load8(a, t, c0, r.v);
+    if (a.mask_in) r.word = a.mask_in[(size_t)t * ((a.K + 31) >> 5) + (c0 >> 5)];
+    else if (a.score_f) load8f(a.f + c0, r.f);
 }
 
-// Kept values of this lane's 8 channels (a warp: 256 channels from a multiple
-// of 256 on; act: below K), selected here unless mask_in.
-__device__ __forceinline__ void df_keep8(const StageArgs &a, int t, int c0, bool act, float eta, float (&xh)[8])
+// Kept values, selected here unless mask_in.
+__device__ __forceinline__ void df_keep8(const StageArgs &a, const DfRaw &r, int t, int c0, bool act, float eta,
+                                         float (&xh)[8])
 {
     const int lane = threadIdx.x & 31, words = (a.K + 31) >> 5;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, f[8], sc[8];
-    if (act) df_load8(a, t, c0, v);
-    const bool has_f = a.score_f && act && !a.mask_in;
-    if (has_f) load8f(a.f + c0, f);
-    score8(v, a.dpts, eta, has_f ? f : nullptr, 0, xh, sc);
+    float sc[8];
+    score8(r.v, a.dpts, eta, nullptr, 0, xh, sc);
     uint32_t keep;
     if (a.mask_in) {
-        keep = act ? (a.mask_in[(size_t)t * words + (c0 >> 5)] >> (8 * (lane & 3))) & 0xFFu : 0u;
+        keep = (r.word >> (8 * (lane & 3))) & 0xFFu;
     } else {
+        if (a.score_f) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sc[e] = __fmul_rn(sc[e], r.f[e]);
+        }
         keep = a.sel == AS_SEL_NM ? nm_keep_dispatch(sc, lane, a.n, a.m)
                                   : (a.sel == AS_SEL_THRESH ? keep_thresh(sc, a.tau) : 0xFFu);
         if (!act) keep = 0;
@@ -227,52 +239,50 @@ __device__ __forceinline__ void df_parts8(const StageArgs &a, int t, int c0, int
     // a block that holds an infinity or a NaN takes the NaN scale, and with it
     // the outputs
     const bool bad = top >= F32_INF_BITS;
-    const int row0 = t * a.P;
+    float S = FMT == AS_FP4_NV ? pow2f(e0) : 1.0f, sv;
+    uint32_t byte;
+    if constexpr (FMT == AS_FP4_NV) {
+        // up to the next of 4 significant bits, or of 2^-9 below the normal numbers
+        const float q = __uint_as_float(top) * pow2f(-e0) * (1.0f / 6.0f);
+        if (q >= 0.015625f) {
+            const uint32_t r = min((__float_as_uint(q) + 0xFFFFFu) & 0xFFF00000u, __float_as_uint(448.0f));
+            sv = __uint_as_float(r);
+            byte = (r >> 20) - 8 * 120;
+        } else {
+            byte = (uint32_t)ceilf(q * 512.0f);
+            sv = (float)byte * (1.0f / 512.0f);
+        }
+        if (bad) byte = 127u;
+    } else {
+        // up to the next power of two (normal ones): one more than the
+        // quantiser's where the mantissa is above 1.5
+        byte = (uint32_t)min(max((int)(top >> 23) - 2 + ((top & 0x7FFFFFu) > 0x400000u ? 1 : 0), 1), 253);
+        sv = __uint_as_float(byte << 23);
+        if (bad) byte = 255u;
+    }
+    float back = __fmul_rn(sv, S), fwd = bad || top == 0u || !(back > 0.0f) ? 0.0f : __fdividef(1.0f, back);
+    if (bad) back = 0.0f;
     uint8_t *sfb = sf + (blk >> 2) * 512 + (blk & 3);
     const bool sf_lane = write && (lane & (LANES - 1)) == 0;
 #pragma unroll 2
     for (int p = 0; p < a.P; ++p) {
-        float am = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) am = fmaxf(am, fabsf(xh[k]));
-#pragma unroll
-        for (int o = 1; o < LANES; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-        // Any scale and any of two codes next to a border will do here, the rest
-        // follows them: no exact divisions.
-        int byte;
-        uint32_t sbits;  // the whole scale
-        if constexpr (FMT == AS_FP4_NV) {
-            // am / 6 rounded to 4 significant bits; below E4M3's normal numbers
-            // the block waits for a part with a smaller row scale
-            sbits = (__float_as_uint(am * (1.0f / 6.0f)) + 0x80000u) & 0xFFF00000u;
-            byte = (int)(sbits >> 20) - 8 * (max(e0 - 2 * p, -126) + 120);
-            if (byte < 8) byte = 0, sbits = 0u;
-            if (byte > 126) byte = 126, sbits = (uint32_t)(126 + 8 * (max(e0 - 2 * p, -126) + 120)) << 20;
-            if (bad) byte = 127;
-        } else {
-            // the smallest power of two that leaves no value above 6: one more
-            // than the quantiser's where the mantissa is above 1.5
-            const uint32_t m = __float_as_uint(am);
-            byte = min(max((int)(m >> 23) - 2 + ((m & 0x7FFFFFu) > 0x400000u ? 1 : 0), 1), 253);  // normal powers of two
-            sbits = (uint32_t)byte << 23;
-            if (bad) byte = 255;
-        }
-        const float back = __uint_as_float(sbits);
-        const float fwd = sbits ? __fdividef(1.0f, back) : 0.0f;
         uint32_t codes = 0u;
 #pragma unroll
         for (int k = 0; k < 4; ++k) codes |= e2m1x2(xh[2 * k] * fwd, xh[2 * k + 1] * fwd) << (8 * k);
-        if (bad) codes = 0u;
-        const int row = row0 + a.P - 1 - p;
-        if (write)
-            *reinterpret_cast<uint32_t *>(img + row * 128 + ((((off >> 4) ^ (row & 7)) << 4) | (off & 15))) = codes;
-        if (sf_lane) sfb[(row >> 7) * C::SFB + (row & 31) * 16 + ((row >> 5) & 3) * 4] = (uint8_t)byte;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // the rest, exact: code * scale has at most 7 bits
+        for (int k = 0; k < 4; ++k) {  // the rest (one rounding)
             const float2 q = e2m1x2_value((codes >> (8 * k)) & 0xFFu);
             xh[2 * k] = fmaf(-q.x, back, xh[2 * k]);
             xh[2 * k + 1] = fmaf(-q.y, back, xh[2 * k + 1]);
         }
+        const int row = t * a.P + a.P - 1 - p;
+        if (write)
+            *reinterpret_cast<uint32_t *>(img + row * 128 + ((((off >> 4) ^ (row & 7)) << 4) | (off & 15))) =
+                bad ? 0u : codes;
+        if (sf_lane) sfb[(row >> 7) * C::SFB + (row & 31) * 16 + ((row >> 5) & 3) * 4] = (uint8_t)byte;
+        S = df_next_scale(S);
+        back = bad ? 0.0f : __fmul_rn(sv, S);
+        fwd = fminf(fwd * 6.0f, 3e38f);  // finite: 0 * fwd stays 0
     }
 }
 
@@ -301,13 +311,25 @@ __global__ void __launch_bounds__(DS_WARPS * 32) k_fp4_stage(StageArgs a)
     float eta = df_given_eta(a, t);
     uint32_t top = 0;
     const bool mean = a.dpts == AS_PTS_DYNAMIC && !a.mask_in;
+    // a warp's first tile stays in registers (it is the only one up to K =
+    // 16384): later loads would queue behind the decode kernel's weights
+    DfRaw raw;
+    {
+        const int c0 = 256 * (kb0 + warp) + 8 * lane;
+        df_load_raw(a, t, c0, kb0 + warp < kb1 && c0 < a.K, raw);
+    }
     if (mean || FMT == AS_FP4_NV) {  // uniform over the cluster
         double sum = 0.0;
         for (int kb = kb0 + warp; kb < kb1; kb += warps) {
             const int c0 = 256 * kb + 8 * lane;
             if (c0 < a.K) {
                 float v[8];
-                df_load8(a, t, c0, v);
+                if (kb == kb0 + warp) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = raw.v[e];
+                } else {
+                    df_load8(a, t, c0, v);
+                }
                 if (mean)
                     sum += (((double)v[0] + (double)v[1]) + ((double)v[2] + (double)v[3])) +
                            (((double)v[4] + (double)v[5]) + ((double)v[6] + (double)v[7]));
@@ -345,13 +367,19 @@ __global__ void __launch_bounds__(DS_WARPS * 32) k_fp4_stage(StageArgs a)
         if (mean) eta = (float)(sum / (double)a.K);
     }
     const int e0 = df_exponent<FMT>(top, eta);
-    if (rank == 0 && (int)threadIdx.x < a.P)
-        a.scale[t * a.P + a.P - 1 - threadIdx.x] = df_part_scale<FMT>(e0, threadIdx.x);
+    if (rank == 0 && threadIdx.x == 0) {
+        float S = FMT == AS_FP4_NV ? pow2f(e0) : 1.0f;
+        for (int p = 0; p < a.P; ++p) {
+            a.scale[t * a.P + a.P - 1 - p] = S;
+            S = df_next_scale(S);
+        }
+    }
     if (rank == 0 && threadIdx.x == 0 && a.dpts && !a.mask_in) a.eta[t] = eta;
     for (int kb = kb0 + warp; kb < kb1; kb += warps) {
         const int c0 = 256 * kb + 8 * lane;
         float xh[8];
-        df_keep8(a, t, c0, c0 < a.K, eta, xh);
+        if (kb != kb0 + warp) df_load_raw(a, t, c0, c0 < a.K, raw);
+        df_keep8(a, raw, t, c0, c0 < a.K, eta, xh);
         uint8_t *img = a.xq + (size_t)kb * a.xb;
         df_parts8<FMT>(a, t, c0, e0, xh, img, img + (size_t)a.N * 128);
     }
@@ -541,13 +569,8 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
         const uint32_t to = mapa_u32(smem_u32(recv + (size_t)rank * a.T * width + o - first_of(owner)), (uint32_t)owner);
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
         const bool some = ok && kb1 > kb0;
-        if (FMT == AS_FP4_NV) {
-            if (a.P == 7) df_send<7>(acc, some, a.T, width, s_scale, to);
-            else df_send<10>(acc, some, a.T, width, s_scale, to);
-        } else {
-            if (a.P == 8) df_send<8>(acc, some, a.T, width, s_scale, to);
-            else df_send<11>(acc, some, a.T, width, s_scale, to);
-        }
+        if (a.P == DF_PARTS_BF16) df_send<DF_PARTS_BF16>(acc, some, a.T, width, s_scale, to);
+        else df_send<DF_PARTS_F32>(acc, some, a.T, width, s_scale, to);
         tc_fence_before();
     }
     __syncwarp();
@@ -620,10 +643,10 @@ static cudaError_t launch_df_fmt(const DecodeFp4Args &a, const StageArgs &s, cud
     if (a.N <= 32) return launch_df<FMT, 32>(a, st);
     if (a.N <= 64) return launch_df<FMT, 64>(a, st);
     if (a.N <= 128) return launch_df<FMT, 128>(a, st);
-    return launch_df<FMT, 192>(a, st);
+    return launch_df<FMT, 160>(a, st);
 }
 
-static int df_parts(int fmt, bool out_bf16) { return fmt == AS_FP4_NV ? (out_bf16 ? 7 : 10) : (out_bf16 ? 8 : 11); }
+static int df_parts(bool out_bf16) { return out_bf16 ? DF_PARTS_BF16 : DF_PARTS_F32; }
 static int df_cols(int T, int parts) { return (T * parts + 15) / 16 * 16; }
 static size_t df_xbytes(int N, int fmt) { return (size_t)N * 128 + (size_t)((N + 127) / 128) * (fmt == AS_FP4_NV ? 2048 : 1024); }
 
@@ -631,13 +654,8 @@ static size_t df_xbytes(int N, int fmt) { return (size_t)N * 128 + (size_t)((N +
 DecodeFp4Layout decode_fp4_layout(int T, int K, int out_bf16)
 {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    size_t xb = 0;
-    int n = 0;
-    for (int fmt : {AS_FP4_MX, AS_FP4_NV}) {
-        const int N = df_cols(T, df_parts(fmt, out_bf16));
-        n = std::max(n, N);
-        xb = std::max(xb, df_xbytes(N, fmt));
-    }
+    const int n = df_cols(T, df_parts(out_bf16));
+    const size_t xb = df_xbytes(n, AS_FP4_NV);
     DecodeFp4Layout l{};
     l.eta = up((size_t)T * ((K + 31) / 32) * sizeof(uint32_t));
     l.scale = l.eta + up((size_t)T * sizeof(float));
@@ -650,7 +668,7 @@ cudaError_t launch_decode_fp4(DecodeFp4Args a, const SelectArgs &sel, bool selec
 {
     const DecodeFp4Layout l = decode_fp4_layout(a.T, a.K, a.out_bf16);
     char *w = static_cast<char *>(ws);
-    a.P = df_parts(fmt, a.out_bf16);
+    a.P = df_parts(a.out_bf16);
     a.N = df_cols(a.T, a.P);
     a.rowf = reinterpret_cast<const float *>(a.Wd + (size_t)df_mtiles(a.n_out) * df_kblocks(a.K) * df_unit(fmt));
     a.scale = reinterpret_cast<const float *>(w + l.scale);
