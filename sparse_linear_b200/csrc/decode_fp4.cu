@@ -300,7 +300,6 @@ template <int FMT>
 __global__ void __launch_bounds__(DS_WARPS * 32) k_fp4_stage(StageArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // after the wait: see k_select_nm_decode
     __shared__ double w_sum[DS_WARPS];
     __shared__ uint32_t w_max[DS_WARPS];
     __shared__ __align__(8) uint64_t c_sum[8], c_max[8];  // of every CTA
@@ -318,6 +317,8 @@ __global__ void __launch_bounds__(DS_WARPS * 32) k_fp4_stage(StageArgs a)
         const int c0 = 256 * (kb0 + warp) + 8 * lane;
         df_load_raw(a, t, c0, kb0 + warp < kb1 && c0 < a.K, raw);
     }
+    // after the wait (see k_select_nm_decode) and after those loads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (mean || FMT == AS_FP4_NV) {  // uniform over the cluster
         double sum = 0.0;
         for (int kb = kb0 + warp; kb < kb1; kb += warps) {
@@ -398,10 +399,13 @@ struct DfCfg {
     static constexpr int W = DF_WTILE, SA = Fp4Cfg<FMT>::SFB;
     static constexpr int XB = NB * 128 + NSB * Fp4Cfg<FMT>::SFB;
     static constexpr int SCOLS = 4 * (1 + NSB) * Fp4Cfg<FMT>::SFT;
-    static constexpr int STAGES = NB <= 32 ? 8 : (NB <= 64 ? 7 : (NB <= 128 ? 5 : 4));
+    // up to 64 columns two CTAs fit an SM, of one call or of two in a row
+    static constexpr int PER_SM = NB <= 64 ? 2 : 1;
+    static constexpr int STAGES = NB <= 32 ? 4 : (NB <= 64 ? 3 : (NB <= 128 ? 5 : 4));
+    static constexpr uint32_t TCOLS = PER_SM == 2 ? 256 : 512;
     static constexpr size_t smem = 1024 + (size_t)STAGES * (W + SA + XB) + 256;
-    static_assert(smem + 12 * 1024 <= 227 * 1024, "shared memory");
-    static_assert(NB + STAGES * SCOLS <= 512, "tensor memory");
+    static_assert(smem + 12 * 1024 <= 227 * 1024 / PER_SM, "shared memory");
+    static_assert(NB + STAGES * SCOLS <= TCOLS, "tensor memory");
 };
 constexpr int DF_RECV = 16 * (128 + 8);  // floats: T outputs' shares from up to 8 CTAs
 
@@ -415,29 +419,36 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
 template <int P>
 __device__ __forceinline__ void df_send(uint32_t acc, bool some, int T, int width, const float *scale, uint32_t to)
 {
-    for (int t = 0; t < T; ++t) {
-        uint32_t r[16];  // columns past P belong to others and are not used
+    for (int t0 = 0; t0 < T; t0 += 2) {
+        uint32_t r[2][16];  // columns past P, and of a token T, belong to others and are not used
         if (some) {
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                  "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                : "r"(acc + (uint32_t)(t * P)));
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                    "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                    : "=r"(r[u][0]), "=r"(r[u][1]), "=r"(r[u][2]), "=r"(r[u][3]), "=r"(r[u][4]), "=r"(r[u][5]),
+                      "=r"(r[u][6]), "=r"(r[u][7]), "=r"(r[u][8]), "=r"(r[u][9]), "=r"(r[u][10]), "=r"(r[u][11]),
+                      "=r"(r[u][12]), "=r"(r[u][13]), "=r"(r[u][14]), "=r"(r[u][15])
+                    : "r"(acc + (uint32_t)((t0 + u) * P)));
             tmem_ld_wait();
         } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = 0u;
+            for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0u;
         }
-        float v = 0.0f;
 #pragma unroll
-        for (int p = 0; p < P; ++p) v = fmaf(__uint_as_float(r[p]), scale[t * P + p], v);
-        st_cluster_f32(to + 4u * (uint32_t)(t * width), v);
+        for (int u = 0; u < 2; ++u) {
+            if (t0 + u >= T) break;
+            float v = 0.0f;
+#pragma unroll
+            for (int p = 0; p < P; ++p) v = fmaf(__uint_as_float(r[u][p]), scale[(t0 + u) * P + p], v);
+            st_cluster_f32(to + 4u * (uint32_t)((t0 + u) * width), v);
+        }
     }
 }
 
 template <int FMT, int NB>
-__global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
+__global__ void __launch_bounds__(DF_THREADS, DfCfg<FMT, NB>::PER_SM) k_decode_fp4(DecodeFp4Args a)
 {
     using C = Fp4Cfg<FMT>;
     using P = DfCfg<FMT, NB>;
@@ -470,7 +481,7 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, 512);
+        tmem_alloc(tmem_slot, P::TCOLS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -577,9 +588,11 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
     cluster_sync_all();
     tc_fence_after();
     const int o0 = first_of(rank), no = first_of(rank + 1) - o0;
-    for (int i = threadIdx.x; i < a.T * no; i += DF_THREADS) {
-        const int t = i / no, c = i % no, o = mt * DF_ROWS + o0 + c;
-        if (o >= a.n_out || !as_in((long long)t * a.n_out + o, (long long)a.T * a.n_out)) continue;
+    const int t1 = (int)threadIdx.x / no, c = (int)threadIdx.x - t1 * no, tstep = max(1, DF_THREADS / no);
+    const int o = mt * DF_ROWS + o0 + c;
+    if (t1 < tstep && o < a.n_out)
+    for (int t = t1; t < a.T; t += tstep) {
+        if (!as_in((long long)t * a.n_out + o, (long long)a.T * a.n_out)) continue;
         float s = 0.0f;
         for (int r = 0; r < nranks; ++r) s += recv[(r * a.T + t) * width + c];
         s *= s_rowf[o0 + c];
@@ -587,7 +600,7 @@ __global__ void __launch_bounds__(DF_THREADS, 1) k_decode_fp4(DecodeFp4Args a)
         if (a.out_bf16) static_cast<__nv_bfloat16 *>(a.y)[(size_t)t * a.n_out + o] = __float2bfloat16_rn(s);
         else static_cast<float *>(a.y)[(size_t)t * a.n_out + o] = s;
     }
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc(tmem, P::TCOLS);
 }
 
 // ---------------------------------------------------------------- host side
@@ -609,11 +622,11 @@ static void df_launch(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 g
     cfg.numAttrs = ranks > 0 ? 2 : 1;
 }
 
-// CTAs of a cluster: as many as fill the GPU (one per SM), at most one per K
+// CTAs of a cluster: as many as fill the GPU, at most one per K
 // block and the portable cluster size.
-static int df_ranks(int K, int n_out)
+static int df_ranks(int K, int n_out, int per_sm)
 {
-    return std::max(1, std::min({sm_count() / df_mtiles(n_out), 8, df_kblocks(K)}));
+    return std::max(1, std::min({per_sm * sm_count() / df_mtiles(n_out), 8, df_kblocks(K)}));
 }
 
 template <int FMT, int NB>
@@ -623,7 +636,7 @@ static cudaError_t launch_df(const DecodeFp4Args &a, cudaStream_t st)
     static int done[64];
     const cudaError_t e = smem_limit_once(k_decode_fp4<FMT, NB>, P::smem, done);
     if (e != cudaSuccess) return e;
-    const int ranks = df_ranks(a.K, a.n_out);
+    const int ranks = df_ranks(a.K, a.n_out, P::PER_SM);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     df_launch(cfg, attr, dim3(ranks, df_mtiles(a.n_out)), DF_THREADS, P::smem, ranks, st);
