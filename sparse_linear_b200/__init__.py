@@ -417,7 +417,8 @@ def as_linear_prefill_nm_split(sel: as_select_out, T: int, W, cfg: as_config, y,
 # These calls are a few microseconds on the GPU, so their checks are too: one
 # pass over each tensor, sizes computed here rather than through the library.
 _U8, _F32, _BF16, _I32 = torch.uint8, torch.float32, torch.bfloat16, torch.int32
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # of a device index
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # a device tensor exists by then
 
 
 def _device(t) -> int:
@@ -426,7 +427,7 @@ def _device(t) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError("libactsparse takes device tensors; got a CPU tensor")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"tensor on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
     return dev
 

@@ -427,6 +427,20 @@ def test_norm_fp4(sl, T, D, fmt):
     check_norm(sl, T, D, "f", "b", "f", "channel", fmt=fmt)
 
 
+@pytest.mark.parametrize("T,D,types,gate,fmt", [
+    (1300, 2056, "bbb", "channel", None), (1300, 2080, "fbf", "token", o.NV), (1201, 4096, "fff", "token", None),
+    (1500, 4128, "bbf", "none", o.MX), (1184, 8192, "ffb", "token", None), (1185, 8192, "bfb", "channel", None)])
+def test_norm_many_rows(sl, T, D, types, gate, fmt):
+    """Enough rows for the persistent kernel."""
+    check_norm(sl, T, D, *types, gate=gate, fmt=fmt)
+
+
+def test_norm_many_rows_options(sl):
+    check_norm(sl, 1300, 4096, "b", "b", "b", "token", inplace=True)
+    check_norm(sl, 1300, 5000, "f", "b", "f", "channel", post=False, scale=-1.5)
+    check_norm(sl, 1300, 4096, "f", "f", "f", "none", weights=False, off=1.0)
+
+
 def test_norm_options(sl):
     check_norm(sl, 5, 1024, "b", "b", "b", "token", inplace=True)
     check_norm(sl, 5, 1024, "f", "f", "f", "channel", post=False, scale=-1.5)
