@@ -113,6 +113,13 @@ __global__ void __launch_bounds__(NT, NT * CH <= 1024 ? 1024 / NT : 1) k_norm_re
         return;
     }
     const size_t row = (size_t)t * D;
+    // one chunk per thread: the weights are loaded with the row, so that their
+    // latency does not follow the reductions
+    float pw[8], qw[8];
+    if constexpr (CH == 1) {
+        if (tid < nch && a.post_w) load8f(a.post_w + 8 * (size_t)tid, pw);
+        if (tid < nch && a.pre_w) load8f(a.pre_w + 8 * (size_t)tid, qw);
+    }
     float v[CH][8];  // r, then r', then h
 #pragma unroll
     for (int r = 0; r < CH; ++r) {
@@ -149,12 +156,11 @@ __global__ void __launch_bounds__(NT, NT * CH <= 1024 ? 1024 / NT : 1) k_norm_re
         for (int r = 0; r < CH; ++r) {
             const int c = r * NT + tid;
             if (c >= nch) continue;
-            float w[8];
-            if (a.post_w) load8f(a.post_w + 8 * (size_t)c, w);
+            if (CH > 1 && a.post_w) load8f(a.post_w + 8 * (size_t)c, pw);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float u = y[r][e] * rms;
-                if (a.post_w) u *= a.w_offset + w[e];
+                if (a.post_w) u *= a.w_offset + pw[e];
                 if (gate) u *= g[r][e];
                 v[r][e] = fmaf(a.res_scale, v[r][e], u);
             }
@@ -173,12 +179,11 @@ __global__ void __launch_bounds__(NT, NT * CH <= 1024 ? 1024 / NT : 1) k_norm_re
     for (int r = 0; r < CH; ++r) {
         const int c = r * NT + tid;
         if (c >= nch) continue;
-        float w[8];
-        if (a.pre_w) load8f(a.pre_w + 8 * (size_t)c, w);
+        if (CH > 1 && a.pre_w) load8f(a.pre_w + 8 * (size_t)c, qw);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             v[r][e] *= rms;
-            if (a.pre_w) v[r][e] *= a.w_offset + w[e];
+            if (a.pre_w) v[r][e] *= a.w_offset + qw[e];
         }
         if (a.h && as_in((long long)row + 8 * c + 7, (long long)T * D))
             store8_any(a.h, row + 8 * (size_t)c, a.h_bf16, v[r]);
@@ -195,7 +200,8 @@ __global__ void __launch_bounds__(NT, NT * CH <= 1024 ? 1024 / NT : 1) k_norm_re
 // registers.  8192 x 8192: 179 us against 215 us for one CTA per row (float32 r
 // and per-token gate, bf16 y and h; 1.07 GB, 6.0 TB/s) and 106 against 165 us
 // (bf16, gate of channels); 8192 x 4096: 90 against 104 and 56 against 80 us.
-// Below 8 rows per SM the ring does not fill; other D keep one CTA per row.
+// From two rows per SM on (300 x 4096: 6.1 against 7.0 us, 1000 x 8192: 18 against
+// 31 us); other D keep one CTA per row.
 constexpr int NR_STAGES = 2;  // at most (one where a row of three float32 inputs fills a third of an SM)
 template <int NT, int CH, int PER_SM>
 __global__ void __launch_bounds__(NT, PER_SM) k_norm_ring(NormArgs a, int T, int D, int kt, int stages)
@@ -336,14 +342,14 @@ static cudaError_t launch_norm_t(const NormArgs &a, int T, int D, cudaStream_t s
 cudaError_t launch_norm(const NormArgs &a, int T, int D, cudaStream_t st)
 {
     const int nch = D / 8;
-    if (a.y && T >= 8 * sm_count()) {
+    if (a.y && T >= 2 * sm_count()) {
         if (nch > 256 && nch <= 512) return launch_norm_ring<256, 2, 3>(a, T, D, st);
         if (nch > 512 && nch <= 1024) return launch_norm_ring<512, 2, 1>(a, T, D, st);
     }
     if (nch <= 128) return launch_norm_t<128, 1>(a, T, D, st);
     if (nch <= 256) return launch_norm_t<256, 1>(a, T, D, st);
-    if (nch <= 512) return launch_norm_t<256, 2>(a, T, D, st);
-    if (nch <= 1024) return launch_norm_t<512, 2>(a, T, D, st);
+    if (nch <= 512) return launch_norm_t<512, 1>(a, T, D, st);
+    if (nch <= 1024) return launch_norm_t<1024, 1>(a, T, D, st);
     if (nch <= 2048) return launch_norm_t<512, 4>(a, T, D, st);
     return launch_norm_t<1024, 4>(a, T, D, st);
 }
