@@ -441,6 +441,56 @@ struct FpFew {
     static_assert(N + STAGES * SCOLS <= 512, "tensor memory");
 };
 
+// The sum of R CTAs' partial tiles, in rank order.  A warp takes a token's 128
+// outputs, 4 per lane, so that its loads cover a peer's row without gaps, and
+// two tokens at a time, with the loads from all peers in flight.  R is a
+// constant: branches on it between the loads cost more than the loads (one
+// CTA, 128 tokens: 6400 clocks).
+template <int N, int RSTR, int R>
+__device__ __forceinline__ void few_sum(const Fp4Params &p, const float *red, const float *s_xs, const float *s_ws,
+                                        int rank, int ot, int tt, int warp, int lane)
+{
+    const int tn = min(N, p.T - tt * N), col = ot * 128 + 4 * lane;
+    constexpr int step = R * (FF_THREADS / 32);
+    const float4 ws = *reinterpret_cast<const float4 *>(s_ws + 4 * lane);
+    for (int t0 = rank * (FF_THREADS / 32) + warp; t0 < tn; t0 += 2 * step) {
+        float4 f[2][R];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float *own = red + min(t0 + k * step, tn - 1) * RSTR + 4 * lane;
+            if constexpr (R == 1) {
+                f[k][0] = *reinterpret_cast<const float4 *>(own);
+            } else if (k == 0 || t0 + k * step < tn) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(f[k][r].x), "=f"(f[k][r].y), "=f"(f[k][r].z), "=f"(f[k][r].w)
+                                 : "r"(mapa_u32(smem_u32(own), (uint32_t)r)));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int t = t0 + k * step, row = tt * N + t;
+            if (t >= tn || col >= p.n_out || !as_in((long long)row * p.n_out + col + 3, (long long)p.T * p.n_out))
+                continue;
+            float4 v = f[k][0];
+#pragma unroll
+            for (int r = 1; r < R; ++r) {
+                v.x += f[k][r].x; v.y += f[k][r].y; v.z += f[k][r].z; v.w += f[k][r].w;
+            }
+            const float xs = s_xs[t];
+            v.x = v.x * xs * ws.x; v.y = v.y * xs * ws.y; v.z = v.z * xs * ws.z; v.w = v.w * xs * ws.w;
+            if (p.out_bf16) {
+                const __nv_bfloat162 h0 = __floats2bfloat162_rn(v.x, v.y), h1 = __floats2bfloat162_rn(v.z, v.w);
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.y) + (size_t)row * p.n_out + col) = make_uint2(
+                    *reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+            } else {
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + (size_t)row * p.n_out + col) = v;
+            }
+        }
+    }
+}
+
 template <int FMT, int N>
 __global__ void __launch_bounds__(FF_THREADS, 1)
     k_gemm_fp4_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -460,6 +510,8 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
     uint64_t *full = bars, *empty = bars + S, *done = bars + 2 * S;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 1);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+    __shared__ float s_xs[N];
+    __shared__ __align__(16) float s_ws[128];  // row scales of the tile
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank(), nranks = gridDim.x;
@@ -548,6 +600,10 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
     const bool some = kb1 > kb0;
     bool ok = true;
     if (warp >= 2) {
+        for (int i = (int)threadIdx.x - 64; i < 128; i += FF_THREADS - 64)
+            s_ws[i] = p.w_scale && ot * 128 + i < p.n_out ? p.w_scale[ot * 128 + i] : 1.0f;
+        for (int i = (int)threadIdx.x - 64; i < N; i += FF_THREADS - 64)
+            s_xs[i] = p.x_scale && tt * N + i < p.T ? p.x_scale[tt * N + i] : 1.0f;
         ok = mbar_wait(done, 0);
         tc_fence_after();
         const int q = warp & 3;
@@ -577,44 +633,16 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
     __syncwarp();
     cluster_sync_all();
     tc_fence_after();
-    // ---- sum over the cluster in rank order; 8 consecutive outputs of a token per thread
-    const int tn = min(N, p.T - tt * N);
-    for (int i = rank * FF_THREADS + (int)threadIdx.x; i < tn * 16; i += nranks * FF_THREADS) {
-        const int t = i >> 4, c = (i & 15) * 8, row = tt * N + t, col = ot * 128 + c;
-        if (col >= p.n_out) continue;
-        const uint32_t at = smem_u32(red + t * P::RSTR + c);
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int r = 0; r < nranks; ++r) {
-            const uint32_t src = mapa_u32(at, (uint32_t)r);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float4 f;
-                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                             : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(src + 16 * k) : "memory");
-                v[4 * k] += f.x; v[4 * k + 1] += f.y; v[4 * k + 2] += f.z; v[4 * k + 3] += f.w;
-            }
-        }
-        if (!as_in((long long)row * p.n_out + col + 7, (long long)p.T * p.n_out)) continue;
-        const float xs = p.x_scale ? p.x_scale[row] : 1.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            v[k] *= xs;
-            if (p.w_scale) v[k] *= p.w_scale[col + k];
-        }
-        if (p.out_bf16) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                w[k] = *reinterpret_cast<const uint32_t *>(&h);
-            }
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.y) + (size_t)row * p.n_out + col) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.y) + (size_t)row * p.n_out + col);
-            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
+    // ---- sum over the cluster and write
+    switch (nranks) {
+    case 1: few_sum<N, P::RSTR, 1>(p, red, s_xs, s_ws, rank, ot, tt, warp, lane); break;
+    case 2: few_sum<N, P::RSTR, 2>(p, red, s_xs, s_ws, rank, ot, tt, warp, lane); break;
+    case 3: few_sum<N, P::RSTR, 3>(p, red, s_xs, s_ws, rank, ot, tt, warp, lane); break;
+    case 4: few_sum<N, P::RSTR, 4>(p, red, s_xs, s_ws, rank, ot, tt, warp, lane); break;
+    case 5: few_sum<N, P::RSTR, 5>(p, red, s_xs, s_ws, rank, ot, tt, warp, lane); break;
+    case 6: few_sum<N, P::RSTR, 6>(p, red, s_xs, s_ws, rank, ot, tt, warp, lane); break;
+    case 7: few_sum<N, P::RSTR, 7>(p, red, s_xs, s_ws, rank, ot, tt, warp, lane); break;
+    default: few_sum<N, P::RSTR, 8>(p, red, s_xs, s_ws, rank, ot, tt, warp, lane); break;
     }
     cluster_sync_all();  // no CTA leaves while another reads its sums
     if (warp == 1) tmem_dealloc(tmem, P::TCOLS);
@@ -689,20 +717,35 @@ static cudaError_t launch_fp4_few(const Fp4GemmArgs &a, cudaStream_t st)
     static int done[64];
     cudaError_t e = smem_limit_once(k_gemm_fp4_few<FMT, N>, P::smem, done);
     if (e != cudaSuccess) return e;
-    int ranks = sm_count() / (p.m_tiles * p.n_tiles);
-    ranks = std::max(1, std::min({ranks, 8, p.k_blocks}));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ranks, p.m_tiles, p.n_tiles);
     cfg.blockDim = dim3(FF_THREADS);
     cfg.dynamicSmemBytes = P::smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    // The largest cluster of which all tiles' are resident at once.  SMs / tiles
+    // is not that: a cluster stays within one GPC, so 16 clusters of 8 need two
+    // waves on 148 SMs (256 x 1024 x 4096: 18.8 us with 8 CTAs, 10.7 with the most that fit).
+    static int fit[9];  // clusters of r CTAs that the device holds, plus one
+    int ranks = std::max(1, std::min(8, p.k_blocks));
+    for (; ranks > 1; --ranks) {
+        if (p.m_tiles * p.n_tiles > sm_count() / ranks) continue;
+        if (!fit[ranks]) {
+            int n = 0;
+            cfg.gridDim = dim3(ranks, 1, 1);
+            attr[0].val.clusterDim.x = ranks;
+            e = cudaOccupancyMaxActiveClusters(&n, k_gemm_fp4_few<FMT, N>, &cfg);
+            if (e != cudaSuccess) return e;
+            fit[ranks] = n + 1;
+        }
+        if (p.m_tiles * p.n_tiles < fit[ranks]) break;
+    }
+    cfg.gridDim = dim3(ranks, p.m_tiles, p.n_tiles);
+    attr[0].val.clusterDim.x = ranks;
     return cudaLaunchKernelEx(&cfg, k_gemm_fp4_few<FMT, N>, mA, mB, mSA, mSB, p);
 }
 
@@ -712,7 +755,14 @@ static cudaError_t launch_fp4_t(const Fp4GemmArgs &a, cudaStream_t st)
     if (a.T <= 16) return launch_fp4_few<FMT, 16>(a, st);
     if (a.T <= 32) return launch_fp4_few<FMT, 32>(a, st);
     if (a.T <= 64) return launch_fp4_few<FMT, 64>(a, st);
-    if (a.T <= 256) return launch_fp4_few<FMT, 128>(a, st);
+    // One wave of 128 x 128 tiles at most: with K split over the SMs left and a
+    // short epilogue it beats 256 x 256 tiles at every length (512 x 1024 x 4096
+    // 7.9 against 16.9 us, 512 x 4096 x 14336 26.3 against 30.5, 128 x 14336 x
+    // 14336 33.8 against 37.8); with a second wave it loses (256 x 14336 x 4096
+    // 27.4 against 20.1, 768 x 4096 x 4096 25.3 against 18.2).
+    // At most 16, 32 or 64 tokens take narrower tiles: fewer bytes and MMAs
+    // (64 x 4096 x 4096 7.6 us as 64 columns, 9.0 as 128; 16 tokens 6.5).
+    if ((long long)((a.T + 127) / 128) * ((a.n_out + 127) / 128) <= sm_count()) return launch_fp4_few<FMT, 128>(a, st);
     return launch_fp4_pair<FMT>(a, st);
 }
 
