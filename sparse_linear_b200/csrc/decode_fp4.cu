@@ -619,14 +619,7 @@ static void df_launch(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 g
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = ranks > 0 ? 2 : 1;
-}
-
-// CTAs of a cluster: as many as fill the GPU, at most one per K
-// block and the portable cluster size.
-static int df_ranks(int K, int n_out, int per_sm)
-{
-    return std::max(1, std::min({per_sm * sm_count() / df_mtiles(n_out), 8, df_kblocks(K)}));
+    cfg.numAttrs = 2;
 }
 
 template <int FMT, int NB>
@@ -636,9 +629,12 @@ static cudaError_t launch_df(const DecodeFp4Args &a, cudaStream_t st)
     static int done[64];
     const cudaError_t e = smem_limit_once(k_decode_fp4<FMT, NB>, P::smem, done);
     if (e != cudaSuccess) return e;
-    const int ranks = df_ranks(a.K, a.n_out, P::PER_SM);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
+    static int fit[9];
+    df_launch(cfg, attr, dim3(1), DF_THREADS, P::smem, 1, st);
+    const int ranks =
+        cluster_that_fits(k_decode_fp4<FMT, NB>, cfg, df_mtiles(a.n_out), P::PER_SM, df_kblocks(a.K), fit);
     df_launch(cfg, attr, dim3(ranks, df_mtiles(a.n_out)), DF_THREADS, P::smem, ranks, st);
     return cudaLaunchKernelEx(&cfg, k_decode_fp4<FMT, NB>, a);
 }

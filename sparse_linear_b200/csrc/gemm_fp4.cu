@@ -701,6 +701,41 @@ static cudaError_t launch_fp4_pair(const Fp4GemmArgs &a, cudaStream_t st)
     return cudaGetLastError();
 }
 
+// CTAs of a cluster: the most (at most 8, the portable size, and one per K
+// block) with which the clusters of all tiles are resident at once.  CTAs that
+// the SMs hold / tiles is not that: a cluster stays within one GPC, so that 16
+// clusters of 8 need two waves on 148 SMs (256 x 1024 x 4096: 18.8 us so, 10.7
+// with the most that fit).  fit[r] keeps the device's answer for r, plus one.
+// With two CTAs per SM the SMs' count decides: the answer counts one per SM,
+// and a cluster that is left over shares SMs (decode, one token, 11008 x 14336:
+// 19.7 us so, 26.9 by the answer).
+template <typename Kernel>
+static int cluster_that_fits(Kernel kernel, cudaLaunchConfig_t cfg, int tiles, int per_sm, int k_blocks, int (&fit)[9])
+{
+    int r = std::max(1, std::min(8, k_blocks));
+    for (; r > 1; --r) {
+        if (tiles > per_sm * sm_count() / r) continue;
+        if (per_sm > 1) break;
+        if (!fit[r]) {
+            cudaLaunchAttribute at{};
+            at.id = cudaLaunchAttributeClusterDimension;
+            at.val.clusterDim.x = r;
+            at.val.clusterDim.y = at.val.clusterDim.z = 1;
+            cfg.gridDim = dim3(r, 1, 1);
+            cfg.attrs = &at;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            fit[r] = n + 1;
+        }
+        if (tiles < fit[r]) break;
+    }
+    return r;
+}
+
 template <int FMT, int N>
 static cudaError_t launch_fp4_few(const Fp4GemmArgs &a, cudaStream_t st)
 {
@@ -727,23 +762,8 @@ static cudaError_t launch_fp4_few(const Fp4GemmArgs &a, cudaStream_t st)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // The largest cluster of which all tiles' are resident at once.  SMs / tiles
-    // is not that: a cluster stays within one GPC, so 16 clusters of 8 need two
-    // waves on 148 SMs (256 x 1024 x 4096: 18.8 us with 8 CTAs, 10.7 with the most that fit).
-    static int fit[9];  // clusters of r CTAs that the device holds, plus one
-    int ranks = std::max(1, std::min(8, p.k_blocks));
-    for (; ranks > 1; --ranks) {
-        if (p.m_tiles * p.n_tiles > sm_count() / ranks) continue;
-        if (!fit[ranks]) {
-            int n = 0;
-            cfg.gridDim = dim3(ranks, 1, 1);
-            attr[0].val.clusterDim.x = ranks;
-            e = cudaOccupancyMaxActiveClusters(&n, k_gemm_fp4_few<FMT, N>, &cfg);
-            if (e != cudaSuccess) return e;
-            fit[ranks] = n + 1;
-        }
-        if (p.m_tiles * p.n_tiles < fit[ranks]) break;
-    }
+    static int fit[9];
+    const int ranks = cluster_that_fits(k_gemm_fp4_few<FMT, N>, cfg, p.m_tiles * p.n_tiles, 1, p.k_blocks, fit);
     cfg.gridDim = dim3(ranks, p.m_tiles, p.n_tiles);
     attr[0].val.clusterDim.x = ranks;
     return cudaLaunchKernelEx(&cfg, k_gemm_fp4_few<FMT, N>, mA, mB, mSA, mSB, p);

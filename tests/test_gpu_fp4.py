@@ -206,6 +206,45 @@ def test_product_nan_scale_stays_in_its_row(sl, T, fmt):
     np.testing.assert_array_equal(nan, want)
 
 
+# more than one wave of 128 x 128 tiles: CTA pairs, ragged on every side, one
+# and several tiles per pair, K from half a stage to more than the ring
+PAIRS = [(1300, 416, 1960), (200, 1312, 9992), (2500, 32, 1032), (777, 2080, 4104), (257, 4128, 8200),
+         (3000, 256, 3208)]
+
+
+@pytest.mark.parametrize("fmt", [o.MX, o.NV])
+@pytest.mark.parametrize("T,K,n_out", PAIRS)
+def test_product_pairs(sl, T, K, n_out, fmt):
+    check_product(sl, T, K, n_out, fmt, torch.float32 if T % 2 else torch.bfloat16)
+
+
+@pytest.mark.parametrize("T,K,n_out,fmt", [
+    (1024, 4096, 128, o.NV), (1000, 544, 1032, o.MX), (1111, 1056, 1024, o.NV), (384, 2048, 768, o.MX),
+    (260, 800, 4096, o.NV)])
+def test_product_one_wave(sl, T, K, n_out, fmt):
+    """128 x 128 tiles at many tokens, clusters of 8 down to 1."""
+    check_product(sl, T, K, n_out, fmt, torch.float32)
+    check_product(sl, T, K, n_out, fmt, torch.bfloat16, scales=False)
+
+
+def test_product_pairs_nan_and_deterministic(sl):
+    T, K, n_out, fmt = 1300, 320, 2056, o.NV
+    xc, xb, xS, _ = random_operand(5, T, K, fmt)
+    wc, wb, wS, _ = random_operand(6, n_out, K, fmt)
+    xb[1, 2], wb[7, 1] = 127, 127
+    ys = []
+    for _ in range(2):
+        y = torch.empty(T, n_out, device="cuda")
+        sl.as_linear_prefill_fp4(dev(xc), dev(o.tile_scales(xb, fmt)), dev(wc), dev(o.tile_scales(wb, fmt)), y,
+                                 x_scale=dev(xS), w_scale=dev(wS), fmt=fmt)
+        ys.append(y)
+    ok(sl)
+    want = torch.zeros(T, n_out, dtype=torch.bool)
+    want[1], want[:, 7] = True, True
+    assert torch.equal(torch.isnan(ys[0]).cpu(), want)
+    assert torch.equal(ys[0].nan_to_num(1e30), ys[1].nan_to_num(1e30))
+
+
 @pytest.mark.parametrize("T", [1, 40, 777])
 def test_product_deterministic(sl, T):
     K, n_out, fmt = 2048, 512, o.NV
@@ -274,8 +313,11 @@ def check_decode(sl, x, wc, wb, wS, fmt, cfg, wd=None, eta_static=None):
     if e is not None:
         ref = ref + e.astype(np.float64)[:, None] * rowsum.astype(np.float64)
         mag = mag + np.abs(e.astype(np.float64)[:, None] * rowsum)
-    # a step per 16 channels and part, eight warps, eight CTAs, factor and
-    # shift; a bf16 output takes x in two parts (2^-17) when shifted or float32
+    # float32 sums: a step per 16 channels and part, the parts, eight CTAs,
+    # factor and shift.  A bf16 output takes x in 7 four-bit parts, which leave
+    # at most 6^-7 / 3 = 2^-19.6 of a block's largest value; kept values are
+    # more than a fifth of it on average, which makes at most 2^-17 of mag.
+    # (float32: 10 parts, 6^-10 / 3 = 2^-27.4, inside the first term.)
     tol = ((3 * K / 16 / 64 + 24 + 3) * 2.0 ** -22 + (2.0 ** -17 if dt == torch.bfloat16 else 0)) * mag
     tol = tol + HALF[dt] * np.abs(ref)
     err = np.abs(f32(y.t).astype(np.float64) - ref)
