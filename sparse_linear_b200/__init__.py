@@ -447,7 +447,7 @@ def _arg(name: str, t, shape, dtype, dev: int):
 
 def _bytes(name: str, t, n: int, dev: int):
     """Address of a uint8 buffer of at least n bytes."""
-    if t.dtype != _U8 or t.numel() < n:
+    if t is None or t.dtype != _U8 or t.numel() < n:
         raise ValueError(f"{name} must hold at least {n} uint8 bytes")
     return _arg(name, t, t.shape, _U8, dev)
 

@@ -7,11 +7,13 @@ points.  It performs no arithmetic of its own.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (AS_BF16, AS_F32, AS_FP4_NV, AS_MODE_24, AS_MODE_DENSE, AS_MODE_SPLIT, AS_OP_AMBER, AS_OP_DECODE,
-               AS_OP_DECODE_FP4, AS_OP_PREFILL, AS_OP_SELECT, AS_OP_WEIGHT_PREP, AS_SCORE_CLACT, AS_SCORE_MAG, AS_SEL_ALL, AS_SEL_NM,
-               as_block_sparsity, as_dequant_fp4, as_fp4_decode_bytes, as_fp4_sf_bytes, as_hybrid_dense_blocks,
+               AS_OP_DECODE_FP4, AS_OP_PREFILL, AS_OP_SELECT, AS_OP_WEIGHT_PREP, AS_SCORE_CLACT, AS_SCORE_MAG,
+               AS_SEL_ALL, AS_SEL_NM, as_block_sparsity, as_dequant_fp4, as_fp4_decode_bytes, as_fp4_sf_bytes, as_hybrid_dense_blocks,
                as_hybrid_workspace, as_linear_decode, as_linear_decode_fp4, as_linear_prefill, as_linear_prefill_fp4,
                as_linear_prefill_hybrid, as_linear_prefill_nm_split, as_linear_prefill_rsparse, as_meta24_words,
                as_prefill_mode, as_quant_fp4,
@@ -228,6 +230,14 @@ class SparseLinear:
         return self.prefill_from(bufs, x.shape[0], stream=stream), bufs
 
 
+def _on(stream):
+    """The stream as torch's current one, so that what a call allocates and
+    drops belongs to the stream that uses it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class Fp4Operand:
     """Device buffers of [rows, K] microscaled 4-bit values: ``codes``, tiled
     scale bytes ``sf`` and the float32 row scale ``scale``."""
@@ -243,7 +253,8 @@ class Fp4Operand:
         return self
 
     def values(self, dtype=torch.float32, stream=None) -> torch.Tensor:
-        out = torch.empty(self.rows, self.K, dtype=dtype, device=self.codes.device)
+        with _on(stream):
+            out = torch.empty(self.rows, self.K, dtype=dtype, device=self.codes.device)
         as_dequant_fp4(self.codes, self.sf, out, self.scale, fmt=self.fmt, stream=stream)
         return out
 
@@ -277,11 +288,14 @@ class Fp4Linear:
     def decode(self, x: torch.Tensor, y: torch.Tensor | None = None, mask_out=None, eta_out=None, colnorm_out=None,
                stream=None) -> torch.Tensor:
         """1 to 16 tokens; x is not quantised."""
+        if self.Wd is None:
+            raise ValueError("this layer has no decode layout (keep_decode=False)")
         T = x.shape[0]
-        if y is None:
-            y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
-        if T not in self._ws:
-            self._ws[T] = workspace(as_workspace_size(AS_OP_DECODE_FP4, T, self.K, self.n_out, self.cfg), x.device)
+        with _on(stream):
+            if y is None:
+                y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
+            if T not in self._ws:
+                self._ws[T] = workspace(as_workspace_size(AS_OP_DECODE_FP4, T, self.K, self.n_out, self.cfg), x.device)
         as_linear_decode_fp4(x, self.Wd, self.cfg, y, fmt=self.fmt, g=self.g, rowsum=self.rowsum, mask_out=mask_out,
                              eta_out=eta_out, colnorm_out=colnorm_out, workspace=self._ws[T], stream=stream)
         return y
@@ -291,7 +305,8 @@ class Fp4Linear:
         if x.fmt != self.fmt or x.K != self.K:
             raise ValueError("the operand's format and K must be the weight's")
         if y is None:
-            y = torch.empty(x.rows, self.n_out, dtype=self.out_dtype(), device=x.codes.device)
+            with _on(stream):
+                y = torch.empty(x.rows, self.n_out, dtype=self.out_dtype(), device=x.codes.device)
         as_linear_prefill_fp4(x.codes, x.sf, self.weight.codes, self.weight.sf, y, x_scale=x.scale,
                               w_scale=self.weight.scale, fmt=self.fmt, stream=stream)
         return y
@@ -301,15 +316,17 @@ class Fp4Linear:
         if self.cfg.dpts or self.cfg.var:
             raise ValueError("4-bit prefill has no token shift and no VAR")
         T = x.shape[0]
-        if self.cfg.sel != AS_SEL_ALL:
-            key = ("select", T)
-            if key not in self._ws:
-                self._ws[key] = workspace(as_workspace_size(AS_OP_SELECT, T, self.K, self.n_out, self.cfg), x.device)
-            kept = torch.empty_like(x)
-            as_select(x, self.cfg, select_out(x_masked=kept), chan_factor=self.g, workspace=self._ws[key],
-                      stream=stream)
-            x = kept
-        return self.prefill_from(Fp4Operand(T, self.K, self.fmt, x.device).quantise(x, stream), stream=stream)
+        with _on(stream):
+            if self.cfg.sel != AS_SEL_ALL:
+                key = ("select", T)
+                if key not in self._ws:
+                    self._ws[key] = workspace(as_workspace_size(AS_OP_SELECT, T, self.K, self.n_out, self.cfg),
+                                              x.device)
+                kept = torch.empty_like(x)
+                as_select(x, self.cfg, select_out(x_masked=kept), chan_factor=self.g, workspace=self._ws[key],
+                          stream=stream)
+                x = kept
+            return self.prefill_from(Fp4Operand(T, self.K, self.fmt, x.device).quantise(x, stream), stream=stream)
 
 
 __all__ = ["SparseLinear", "Fp4Linear", "Fp4Operand", "workspace", "hybrid_mode", "dense_blocks_for", "AS_F32", "AS_BF16"]

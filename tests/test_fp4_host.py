@@ -232,3 +232,13 @@ def test_binding_refuses_wrong_tensors(lib):
         lib.as_norm_residual(x, y=x[:2], r_out=x)
     with pytest.raises(ValueError):
         lib.as_norm_residual(x, h=x, pre_w=torch.zeros(64, dtype=torch.bfloat16))
+
+
+def test_missing_buffers_are_refused(lib):
+    with pytest.raises(ValueError):
+        lib._bytes("sf", None, 4, 0)
+    from sparse_linear_b200.layer import Fp4Linear
+    layer = object.__new__(Fp4Linear)
+    layer.Wd = None
+    with pytest.raises(ValueError):
+        layer.decode(torch.zeros(1, 64))

@@ -602,3 +602,28 @@ def test_layer(sl, fmt):
     assert (np.abs(f32(y) - q @ wv.T) <= (K / 64 + 12) * 2.0 ** -22 * (np.abs(q) @ np.abs(wv).T)).all()
     with pytest.raises(ValueError):
         Fp4Linear(W.cuda(), sl.config(dpts=True, n=8, m=16), fmt=fmt).prefill(x.cuda())
+
+
+def test_layer_on_a_side_stream(sl):
+    """What the layer allocates within a call belongs to the call's stream: work
+    that the current stream starts meanwhile does not get its memory."""
+    from sparse_linear_b200.layer import Fp4Linear
+    T, K, n_out = 64, 2048, 264
+    x, W = (t.cuda() for t in synth.random_layer(T, K, n_out, seed=9))
+    cfg = sl.config(score=sl.AS_SCORE_WEIGHT, sel=sl.AS_SEL_NM, n=8, m=16, out_dtype=sl.AS_F32)
+    L, M = Fp4Linear(W, cfg, alpha=0.5), Fp4Linear(W, cfg, alpha=0.5)
+    want = [L.prefill(x), L.decode(x[:16]), L.weight.values()]
+    s = torch.cuda.Stream()
+    big = torch.ones(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(20):  # keeps the side stream busy
+            big = big @ big * 2.0 ** -12
+    got = [M.prefill(x, stream=s), M.decode(x[:16], stream=s.cuda_stream), M.weight.values(stream=s)]
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+            for n in (T * K * 2, T * K // 2, sl.as_fp4_sf_bytes(T, K), T * 4) for _ in range(4)]
+    torch.cuda.synchronize()
+    ok(sl)
+    assert len(junk) == 16
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
