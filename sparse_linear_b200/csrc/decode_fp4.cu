@@ -25,7 +25,11 @@
 // and k_decode_fp4, whose weight copies start before the parts are ready.  (One
 // kernel, every CTA making the parts of its own channels, took 15.0 us against
 // 10.7 us for one token at 11008 x 4096: the row's mean and the parts are then
-// computed 32 times over, beside the weight stream.)
+// computed 32 times over, beside the weight stream.)  Calls one after another,
+// bf16 with 8:16, cold weights: 11008 x 4096, one token with the token shift,
+// 12.0 us (25 MB: 2.1 TB/s); 14336 x 4096, 16 tokens, 13.2 us; 14336 x 11008,
+// one token, 19.7 us (89 MB: 4.5 TB/s).  What is not weight stream is the
+// staging (about 5 us), the first loads' latency and the exchange.
 #include "common.cuh"
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -400,6 +404,7 @@ struct DfCfg {
     static constexpr int XB = NB * 128 + NSB * Fp4Cfg<FMT>::SFB;
     static constexpr int SCOLS = 4 * (1 + NSB) * Fp4Cfg<FMT>::SFT;
     // up to 64 columns two CTAs fit an SM, of one call or of two in a row
+    // (one token 12.0 us against 13.1 with one CTA per SM, 11008 x 4096)
     static constexpr int PER_SM = NB <= 64 ? 2 : 1;
     static constexpr int STAGES = NB <= 32 ? 4 : (NB <= 64 ? 3 : (NB <= 128 ? 5 : 4));
     static constexpr uint32_t TCOLS = PER_SM == 2 ? 256 : 512;
