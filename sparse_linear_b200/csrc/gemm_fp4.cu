@@ -205,7 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
         }
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 16);  // 8 epilogue warps in each CTA (the leader's copy is used)
-        mbar_init(drain, 1);
+        mbar_init(drain, 1);  // the leader's last commit
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tmA);
@@ -280,8 +280,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
                 tc_commit_lead<true>(lead, acc_full);
             }
             tc_commit_lead<true>(lead, drain);
-            mbar_wait(drain, 0);
         }
+        // Both CTAs: the commits of the leader arrive at both, so neither
+        // leaves before the last one has arrived.
+        mbar_wait(drain, 0);
     } else if (warp == 14) {
         // ------------------------------------------------ TMA producer of scales
         if (lane == 0) {
