@@ -280,7 +280,20 @@ class Fp4Linear:
         if keep_decode:
             self.Wd = torch.empty(as_fp4_decode_bytes(self.n_out, self.K, fmt), dtype=torch.uint8, device=dev)
             as_weight_prep_fp4(self.weight.codes, self.weight.sf, self.Wd, w_scale=self.weight.scale, fmt=fmt)
-        self._ws = {}
+        self._decode_bytes = {}
+
+    def _scratch(self, op: int, T: int) -> torch.Tensor | None:
+        """Scratch of one call (neither operation needs zeros), on the current
+        stream.  Each call has its own, so that calls on two streams, or graphs
+        replayed at the same time, share nothing but the weights."""
+        if op == AS_OP_DECODE_FP4:
+            key = (T, self.cfg.out_dtype, self.cfg.score)
+            if key not in self._decode_bytes:
+                self._decode_bytes[key] = as_workspace_size(op, T, self.K, self.n_out, self.cfg)
+            n = self._decode_bytes[key]
+        else:
+            n = as_workspace_size(op, T, self.K, self.n_out, self.cfg)
+        return torch.empty(n, dtype=torch.uint8, device=self.g.device) if n else None
 
     def out_dtype(self) -> torch.dtype:
         return torch.bfloat16 if self.cfg.out_dtype == AS_BF16 else torch.float32
@@ -294,10 +307,9 @@ class Fp4Linear:
         with _on(stream):
             if y is None:
                 y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
-            if T not in self._ws:
-                self._ws[T] = workspace(as_workspace_size(AS_OP_DECODE_FP4, T, self.K, self.n_out, self.cfg), x.device)
+            ws = self._scratch(AS_OP_DECODE_FP4, T)
         as_linear_decode_fp4(x, self.Wd, self.cfg, y, fmt=self.fmt, g=self.g, rowsum=self.rowsum, mask_out=mask_out,
-                             eta_out=eta_out, colnorm_out=colnorm_out, workspace=self._ws[T], stream=stream)
+                             eta_out=eta_out, colnorm_out=colnorm_out, workspace=ws, stream=stream)
         return y
 
     def prefill_from(self, x: Fp4Operand, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -318,13 +330,9 @@ class Fp4Linear:
         T = x.shape[0]
         with _on(stream):
             if self.cfg.sel != AS_SEL_ALL:
-                key = ("select", T)
-                if key not in self._ws:
-                    self._ws[key] = workspace(as_workspace_size(AS_OP_SELECT, T, self.K, self.n_out, self.cfg),
-                                              x.device)
                 kept = torch.empty_like(x)
-                as_select(x, self.cfg, select_out(x_masked=kept), chan_factor=self.g, workspace=self._ws[key],
-                          stream=stream)
+                as_select(x, self.cfg, select_out(x_masked=kept), chan_factor=self.g,
+                          workspace=self._scratch(AS_OP_SELECT, T), stream=stream)
                 x = kept
             return self.prefill_from(Fp4Operand(T, self.K, self.fmt, x.device).quantise(x, stream), stream=stream)
 
