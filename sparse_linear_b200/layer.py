@@ -40,6 +40,18 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     return torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
+def _current_stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _on(stream):
+    """The stream as torch's current one, so that what a call allocates and
+    drops belongs to the stream that uses it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class SparseLinear:
     """One activation-sparsified linear layer y = prune(x) W^T.
 
@@ -49,6 +61,10 @@ class SparseLinear:
     ``importance`` picks the channel factor g of the weight-aware score:
     ``"norm"`` (column norm of W) or ``"amber"`` (Amber-Pruner: column norm
     of the standardised weights inside the ``amber_pct`` percentiles).
+
+    Workspaces are kept per stream, so that calls on two streams may run at the
+    same time.  A captured call uses those of the stream it is captured on:
+    graphs captured on one stream are replayed one after another.
     """
 
     def __init__(self, W: torch.Tensor, cfg, alpha: float = 0.0, keep_wt: bool = True,
@@ -75,11 +91,19 @@ class SparseLinear:
                                  bounds=self.amber_bounds, workspace=ws)
         self._ws = {}
 
+    def _kept(self, use: tuple, nbytes: int) -> torch.Tensor:
+        """The current stream's zero-filled workspace of this use and size."""
+        key = (*use, nbytes, _current_stream())
+        ws = self._ws.get(key)
+        if ws is None:
+            ws = workspace(nbytes, self.W.device)
+            # zeros that a capture fills are the graph's: other calls would find them unfilled
+            if not torch.cuda.is_current_stream_capturing():
+                self._ws[key] = ws
+        return ws
+
     def _workspace(self, op: int, T: int) -> torch.Tensor:
-        key = (op, T)
-        if key not in self._ws:
-            self._ws[key] = workspace(as_workspace_size(op, T, self.K, self.n_out, self.cfg), self.W.device)
-        return self._ws[key]
+        return self._kept((op, T), as_workspace_size(op, T, self.K, self.n_out, self.cfg))
 
     def out_dtype(self) -> torch.dtype:
         return torch.bfloat16 if self.cfg.out_dtype == AS_BF16 else torch.float32
@@ -88,11 +112,12 @@ class SparseLinear:
     def decode(self, x: torch.Tensor, y: torch.Tensor | None = None, mask_out=None, eta_out=None,
                colnorm_out=None, stream=None) -> torch.Tensor:
         T = x.shape[0]
-        if y is None:
-            y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
+        with _on(stream):
+            if y is None:
+                y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
+            ws = self._workspace(AS_OP_DECODE, T)
         as_linear_decode(x, self.Wt, self.cfg, y, g=self.g, rowsum=self.rowsum, mask_out=mask_out,
-                         eta_out=eta_out, colnorm_out=colnorm_out,
-                         workspace=self._workspace(AS_OP_DECODE, T), stream=stream)
+                         eta_out=eta_out, colnorm_out=colnorm_out, workspace=ws, stream=stream)
         return y
 
     # ---------------------------------------------------------------- prefill
@@ -125,17 +150,21 @@ class SparseLinear:
                stream=None) -> None:
         T = x.shape[0]
         chan = self.g if self.cfg.score != AS_SCORE_CLACT else None
+        with _on(stream):
+            ws = self._workspace(AS_OP_SELECT, T)
         as_select(x, self.cfg, select_out(**bufs), chan_factor=chan, running_var=running_var,
-                  var_first_batch=first_batch, workspace=self._workspace(AS_OP_SELECT, T), stream=stream)
+                  var_first_batch=first_batch, workspace=ws, stream=stream)
 
     def prefill_from(self, bufs: dict, T: int, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-        if y is None:
-            y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=self.W.device)
+        with _on(stream):
+            if y is None:
+                y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=self.W.device)
+            ws = self._workspace(AS_OP_PREFILL, T)
         as_linear_prefill(select_out(**{k: v for k, v in bufs.items()
                                         if k in ("x_masked", "x_compact", "meta24", "x_masked_lo",
                                                  "x_compact_lo")}),
                           self.W, T, self.cfg, y, rowsum=self.rowsum, eta=bufs.get("eta"),
-                          nu=bufs.get("nu"), workspace=self._workspace(AS_OP_PREFILL, T), stream=stream)
+                          nu=bufs.get("nu"), workspace=ws, stream=stream)
         return y
 
     # ---------------------------------------------------------------- hybrid 2:4
@@ -145,14 +174,13 @@ class SparseLinear:
         busiest 4-channel blocks dense, 2:4 elsewhere.  `bufs` holds this
         layer's 2:4 selection of x (cfg: 2:4 by magnitude)."""
         T = x.shape[0]
-        if y is None:
-            y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
-        key = ("hybrid", T, n_dense)
-        if key not in self._ws:
-            self._ws[key] = workspace(as_hybrid_workspace(T, self.K, self.n_out, n_dense), x.device)
+        with _on(stream):
+            if y is None:
+                y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
+            ws = self._kept(("hybrid", T, n_dense), as_hybrid_workspace(T, self.K, self.n_out, n_dense))
         sel = select_out(**{k: v for k, v in bufs.items() if k in ("bitmask", "x_compact", "meta24")})
         as_linear_prefill_hybrid(sel, x, self.W, y, n_dense, dense_idx=dense_idx, sparsity=sparsity,
-                                 workspace=self._ws[key], stream=stream)
+                                 workspace=ws, stream=stream)
         return y
 
     def prefill_auto(self, x: torch.Tensor, dense_frac: float = 0.05, stream=None):
@@ -164,41 +192,40 @@ class SparseLinear:
                 and self.cfg.score == AS_SCORE_MAG and not self.cfg.dpts and not self.cfg.var):
             raise ValueError("prefill_auto needs a 2:4 magnitude configuration")
         T = x.shape[0]
-        key = ("sparsity", T)
-        if key not in self._ws:
-            self._ws[key] = workspace(as_hybrid_workspace(T, self.K, 0, 0), x.device)
-        sp = torch.empty(1, dtype=torch.float32, device=x.device)
-        as_block_sparsity(x, sp, workspace=self._ws[key], stream=stream)
-        s = float(sp.item())
-        code = as_prefill_mode(s)
-        mode = _MODE_NAMES[code]
-        if code == AS_MODE_DENSE:
-            cfg_all = config(sel=AS_SEL_ALL, out_dtype=self.cfg.out_dtype)
-            y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
-            as_linear_prefill(select_out(x_masked=x), self.W, T, cfg_all, y,
-                              workspace=self._workspace(AS_OP_PREFILL, T), stream=stream)
-            return y, mode, s
-        bufs = self.select_buffers(T, x.device)
-        self.select(x, bufs, stream=stream)
-        if code == AS_MODE_24:
-            return self.prefill_from(bufs, T, stream=stream), mode, s
-        return self.prefill_hybrid_from(x, bufs, as_hybrid_dense_blocks(self.K, dense_frac), stream=stream), mode, s
+        with _on(stream):  # the reading back too
+            sp = torch.empty(1, dtype=torch.float32, device=x.device)
+            as_block_sparsity(x, sp, workspace=self._kept(("sparsity", T), as_hybrid_workspace(T, self.K, 0, 0)),
+                              stream=stream)
+            s = float(sp.item())
+            code = as_prefill_mode(s)
+            mode = _MODE_NAMES[code]
+            if code == AS_MODE_DENSE:
+                cfg_all = config(sel=AS_SEL_ALL, out_dtype=self.cfg.out_dtype)
+                y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
+                as_linear_prefill(select_out(x_masked=x), self.W, T, cfg_all, y,
+                                  workspace=self._workspace(AS_OP_PREFILL, T), stream=stream)
+                return y, mode, s
+            bufs = self.select_buffers(T, x.device)
+            self.select(x, bufs, stream=stream)
+            if code == AS_MODE_24:
+                return self.prefill_from(bufs, T, stream=stream), mode, s
+            return (self.prefill_hybrid_from(x, bufs, as_hybrid_dense_blocks(self.K, dense_frac), stream=stream), mode,
+                    s)
 
     def prefill_rsparse(self, x: torch.Tensor, B: torch.Tensor, A: torch.Tensor, stream=None):
         """Selection + prefill with the R-Sparse compensation of the dropped
         channels (overview page, section 3.3): B [K, r], A [n_out, r] bf16
         factors of W, r in {64, 128}.  Returns (y, bufs)."""
         T = x.shape[0]
-        bufs = self.select_buffers(T, x.device)
+        with _on(stream):
+            bufs = self.select_buffers(T, x.device)
+            ws = self._kept(("rsparse", T, A.shape[1]), as_rsparse_prefill_workspace(T, self.K, A.shape[1]))
+            y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
         self.select(x, bufs, stream=stream)
-        key = ("rsparse", T, A.shape[1])
-        if key not in self._ws:
-            self._ws[key] = workspace(as_rsparse_prefill_workspace(T, self.K, A.shape[1]), x.device)
-        y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=x.device)
         sel = select_out(**{k: v for k, v in bufs.items()
                             if k in ("bitmask", "x_masked", "x_compact", "meta24", "x_masked_lo", "x_compact_lo")})
         as_linear_prefill_rsparse(sel, x, self.W, self.cfg, y, B, A, rowsum=self.rowsum, eta=bufs.get("eta"),
-                                  workspace=self._ws[key], stream=stream)
+                                  workspace=ws, stream=stream)
         return y, bufs
 
     def prefill_nm_split(self, x: torch.Tensor, n_dense: int, running_var=None, first_batch: bool = False,
@@ -209,33 +236,25 @@ class SparseLinear:
         section 3.2).  Returns (y, bufs)."""
         T, K = x.shape
         dev = x.device
-        bufs = self.select_buffers(T, dev)
-        bufs["x_compact"] = torch.empty(T, K // 2, dtype=torch.bfloat16, device=dev)
-        bufs["meta24"] = torch.empty(as_meta24_words(T, K), dtype=torch.int32, device=dev)
-        bufs["bitmask24"] = torch.empty(T, (K + 31) // 32, dtype=torch.int32, device=dev)
+        with _on(stream):
+            bufs = self.select_buffers(T, dev)
+            bufs["x_compact"] = torch.empty(T, K // 2, dtype=torch.bfloat16, device=dev)
+            bufs["meta24"] = torch.empty(as_meta24_words(T, K), dtype=torch.int32, device=dev)
+            bufs["bitmask24"] = torch.empty(T, (K + 31) // 32, dtype=torch.int32, device=dev)
+            ws = self._kept(("hybrid", T, n_dense), as_hybrid_workspace(T, K, self.n_out, n_dense))
+            y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=dev)
         self.select(x, bufs, running_var=running_var, first_batch=first_batch, stream=stream)
-        key = ("hybrid", T, n_dense)
-        if key not in self._ws:
-            self._ws[key] = workspace(as_hybrid_workspace(T, K, self.n_out, n_dense), dev)
-        y = torch.empty(T, self.n_out, dtype=self.out_dtype(), device=dev)
         sel = select_out(**{k: v for k, v in bufs.items() if k in ("x_masked", "x_compact", "meta24", "bitmask24")})
         as_linear_prefill_nm_split(sel, T, self.W, self.cfg, y, n_dense, rowsum=self.rowsum, eta=bufs.get("eta"),
                                    nu=bufs.get("nu"), dense_idx=dense_idx, sparsity=sparsity,
-                                   workspace=self._ws[key], stream=stream)
+                                   workspace=ws, stream=stream)
         return y, bufs
 
     def prefill(self, x: torch.Tensor, running_var=None, first_batch: bool = False, stream=None):
-        bufs = self.select_buffers(x.shape[0], x.device)
+        with _on(stream):
+            bufs = self.select_buffers(x.shape[0], x.device)
         self.select(x, bufs, running_var=running_var, first_batch=first_batch, stream=stream)
         return self.prefill_from(bufs, x.shape[0], stream=stream), bufs
-
-
-def _on(stream):
-    """The stream as torch's current one, so that what a call allocates and
-    drops belongs to the stream that uses it."""
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 class Fp4Operand:

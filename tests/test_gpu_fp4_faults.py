@@ -102,3 +102,31 @@ def test_layer_with_another_configuration(sl):  # noqa: F811
         assert torch.equal(L.decode(x), Fp4Linear(W, cfg).decode(x))
         assert torch.equal(L.prefill(x), Fp4Linear(W, cfg).prefill(x))
     ok(sl)
+
+
+def test_one_sparse_layer_on_two_streams(sl):  # noqa: F811
+    """SparseLinear: decode and prefill of different tokens on two streams behind
+    other work, and the mode switch, which reads a result back."""
+    from sparse_linear_b200.layer import SparseLinear
+    T, K, n_out = 8, 2048, 520
+    _, W = synth.random_layer(T, K, n_out, seed=34)
+    xs = [synth.random_layer(T, K, n_out, seed=60 + i)[0].cuda() for i in range(8)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for cfg, calls in ((sl.config(sel=sl.AS_SEL_NM, n=8, m=16, dpts=True, out_dtype=sl.AS_F32), ("decode", "prefill")),
+                       (sl.config(score=sl.AS_SCORE_CLACT, sel=sl.AS_SEL_NM, n=8, m=16), ("decode", "prefill")),
+                       (sl.config(sel=sl.AS_SEL_TOPK, k_keep=900), ("decode",)),
+                       (sl.config(sel=sl.AS_SEL_NM, n=2, m=4), ("prefill_auto",))):
+        L = SparseLinear(W.cuda(), cfg)
+
+        def run(i, **kw):
+            out = [getattr(L, c)(xs[i], **kw) for c in calls]
+            return [v[0] if isinstance(v, tuple) else v for v in out]
+
+        want = [run(i) for i in range(8)]
+        ok(sl)
+        for s in streams:
+            busy(s)
+        got = [run(i, stream=streams[i % 2]) for i in range(8)]
+        ok(sl)
+        for w, g in zip(want, got):
+            assert all(torch.equal(a, b) for a, b in zip(w, g))

@@ -7,7 +7,7 @@ import sparse_linear_b200.layer as layer
 import sparse_linear_b200 as sl
 
 CALLS = ("as_quant_fp4", "as_dequant_fp4", "as_weight_prep", "as_weight_prep_fp4", "as_linear_decode_fp4",
-         "as_linear_prefill_fp4", "as_select")
+         "as_linear_prefill_fp4", "as_select", "as_linear_decode", "as_linear_prefill")
 
 
 @pytest.fixture
@@ -54,3 +54,18 @@ def test_fp4_scratch_follows_the_configuration(calls):
         L.decode(torch.zeros(16, 64))
         need = sl.as_workspace_size(sl.AS_OP_DECODE_FP4, 16, 64, 16, cfg)
         assert given(calls, "as_linear_decode_fp4")[-1].numel() >= need
+
+
+def test_sparse_workspaces_belong_to_a_stream(calls, monkeypatch):
+    """Kept per stream, and not kept when a capture fills them with zeros."""
+    now = [1]
+    monkeypatch.setattr(layer, "_current_stream", lambda: now[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[0] == 3)
+    L = layer.SparseLinear(torch.zeros(16, 64), sl.config(score=sl.AS_SCORE_CLACT, n=8, m=16))
+    for stream in (1, 2, 1, 3, 3):
+        now[0] = stream
+        L.decode(torch.zeros(2, 64))
+        L.prefill(torch.zeros(20, 64))
+    for name in ("as_linear_decode", "as_select", "as_linear_prefill"):
+        one, two, again, captured, next_captured = [w.data_ptr() for w in given(calls, name)]
+        assert one == again and len({one, two, captured, next_captured}) == 4, name
