@@ -588,9 +588,11 @@ as_status as_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const float
  * W the values that Wq stands for.  Scores, selection, shift and the outputs
  * mask_out, eta_out, colnorm_out are those of as_linear_decode.  x is not
  * rounded to 4 bits: a kept value enters the tensor cores as a sum of 4-bit
- * parts, 10 for float32 output and 7 for bf16 output, which leave at most 2^-25
- * or 2^-18 of the largest kept value of its block of 16 or 32 channels
- * (AS_FP4_NV: or of 2^-17 of its token's largest, where that is more).  g and
+ * parts, 10 for float32 output and 8 for bf16 output, which leave at most 2^-28
+ * or 2^-22 of the largest kept value of its block of 16 or 32 channels
+ * (AS_FP4_NV: or of 2^-17 of its token's largest |x| + |shift|, where that is
+ * more).  The bound is one of the block: values far below its largest keep
+ * fewer bits than that one.  g and
  * rowsum describe the same W (as_weight_prep on its values).  A non-finite
  * kept value or weight scale makes the outputs that read it NaN.
  *   x [T, K] in `dt`; K % 32 == 0, n_out % 8 == 0; cfg->var is not supported.

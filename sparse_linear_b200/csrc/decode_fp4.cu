@@ -4,16 +4,22 @@
 // scales (tcgen05.mma kind::mxf4nvf4), with the outputs on the M = 128 side,
 // so that nothing is unpacked and the kernel is bound by the bytes of W.  The
 // kept values of x enter as a sum of P four-bit parts,
-//   xhat m = sum_p S_p s_b code_p  (+ rest),  S_p = S_0 / 6^p,
-// with one scale s_b per block: the smallest E4M3 value (NV) or power of two
-// (MX) that leaves no value of the block above 6.  A code errs by at most half
-// the largest step of E2M1, 1, so that what a part leaves is at most 6 for the
-// next; P parts leave at most s_b S_0 / 6^P.  float32 output takes 10 parts,
-// which leave below 2^-25 of the block's largest value; bf16 output takes 7:
-// below 2^-18, far inside the output's half step of 2^-8.  S_p is a rounded
-// float32, which a value feels as one more rounding of 2^-24.  Each part of
-// each token is a column of the product (T P <= 160 of at most 256) and the
-// epilogue adds a token's columns in float32.
+//   xhat m = S sum_p s_b 8^-p code_p  (+ rest),
+// with a power of two S per token (MX: 1) and one scale s_b per block: the
+// smallest E4M3 value (NV) or power of two (MX) that leaves no value of the
+// block above 4 s_b S.  Up to 4 the codes' steps are at most 1, so that a part
+// leaves at most 1/2, which is 4 for the next one: P parts leave at most
+// s_b S 8^-(P-1) / 2.  MX: s_b is below half the block's largest value M (its
+// smallest scale is 2^-126).  NV: s_b S is at most 9/32 M, and for scales among
+// E4M3's subnormals at most M/4 + 2^-9 S with S < amax/896 of the token's
+// largest, below 0.54 M where M is at least 2^-17 amax.  So P parts leave at
+// most 0.27 8^-(P-1) M: 8 parts for bf16 output 2^-22 M, 10 parts for float32
+// output 2^-28 M.  All factors are powers of two: only the parts themselves
+// and their sum in the epilogue round.  Each part of each token is a column of the
+// product (T P <= 160 of at most 256); the epilogue adds a token's columns in
+// float32, smallest first.
+//   (Powers of 6 with the block's largest value at 6 were used first, 7 and 10
+// parts: 2^-17.7 M and 2^-25.5 M, with a rounded factor per part.)
 //   Every channel's codes are read.  Reading only the rows of kept channels
 // was built first (channel-major codes, cp.async, unpacking for mma.sync):
 // 8:16 with one token halves the bytes, but the unpacking bound it: 14.5 us a
@@ -40,7 +46,7 @@ namespace as {
 constexpr int DF_ROWS = 128;  // outputs per tile
 constexpr int DF_KB = 256;    // channels per stage
 constexpr int DF_WTILE = DF_ROWS * DF_KB / 2;
-constexpr int DF_PARTS_BF16 = 7, DF_PARTS_F32 = 10;  // by the output's type
+constexpr int DF_PARTS_BF16 = 8, DF_PARTS_F32 = 10;  // by the output's type
 
 static int df_kblocks(int K) { return (K + DF_KB - 1) / DF_KB; }
 static int df_mtiles(int n_out) { return (n_out + DF_ROWS - 1) / DF_ROWS; }
@@ -153,7 +159,7 @@ struct StageArgs {
     const float *eta_in;
     uint32_t *mask;  // keep words, written unless mask_in
     float *eta;      // [T], written unless mask_in (with a shift)
-    float *scale;    // [N] row scale of every column
+    float *scale;    // [T] S of every token
     uint8_t *xq;     // the columns' images, xb bytes per K block
     size_t xb;
 };
@@ -166,15 +172,16 @@ __device__ __forceinline__ void df_load8(const StageArgs &a, int t, int c0, floa
     else load8(static_cast<const float *>(a.x) + at, v);
 }
 
-// Exponent of S_0: |x - eta| is at most top + |eta|.
+// Exponent of S: the smallest e >= -126 with m <= 4 * 448 * 2^e for the token's
+// largest possible |x - eta|, m = top + |eta|.  1792 = 1.75 * 2^10.
 template <int FMT>
 __device__ __forceinline__ int df_exponent(uint32_t top, float eta)
 {
     if (FMT == AS_FP4_MX) return 0;
-    return nv_row_exponent(min(__float_as_uint(__uint_as_float(top) + fabsf(eta)), F32_INF_BITS - 1u));
+    const uint32_t m = min(__float_as_uint(__uint_as_float(top) + fabsf(eta)), F32_INF_BITS - 1u);
+    if (m == 0u) return 0;
+    return max((int)(m >> 23) - 127 - 10 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);
 }
-// Row scale of the next part; the same rounding wherever it is formed.
-__device__ __forceinline__ float df_next_scale(float S) { return __fmul_rn(S, 1.0f / 6.0f); }
 
 // What a lane needs of its 8 channels (a warp: 256 channels from a multiple of
 // 256 on; act: below K).
@@ -243,11 +250,12 @@ __device__ __forceinline__ void df_parts8(const StageArgs &a, int t, int c0, int
     // a block that holds an infinity or a NaN takes the NaN scale, and with it
     // the outputs
     const bool bad = top >= F32_INF_BITS;
-    float S = FMT == AS_FP4_NV ? pow2f(e0) : 1.0f, sv;
+    float sv = 1.0f;  // scale in units of 2^e (NV: S, MX: the block's own)
+    int e = e0;
     uint32_t byte;
     if constexpr (FMT == AS_FP4_NV) {
         // up to the next of 4 significant bits, or of 2^-9 below the normal numbers
-        const float q = __uint_as_float(top) * pow2f(-e0) * (1.0f / 6.0f);
+        const float q = __uint_as_float(top) * pow2f(-e0) * 0.25f;
         if (q >= 0.015625f) {
             const uint32_t r = min((__float_as_uint(q) + 0xFFFFFu) & 0xFFF00000u, __float_as_uint(448.0f));
             sv = __uint_as_float(r);
@@ -258,14 +266,18 @@ __device__ __forceinline__ void df_parts8(const StageArgs &a, int t, int c0, int
         }
         if (bad) byte = 127u;
     } else {
-        // up to the next power of two (normal ones): one more than the
-        // quantiser's where the mantissa is above 1.5
-        byte = (uint32_t)min(max((int)(top >> 23) - 2 + ((top & 0x7FFFFFu) > 0x400000u ? 1 : 0), 1), 253);
-        sv = __uint_as_float(byte << 23);
+        // up to the next power of two (normal ones): the quantiser's, or twice
+        // that for a largest value that is no power of two
+        byte = (uint32_t)min(max((int)(top >> 23) - 2 + ((top & 0x7FFFFFu) != 0u ? 1 : 0), 1), 253);
+        e = (int)byte - 127;
         if (bad) byte = 255u;
     }
-    float back = __fmul_rn(sv, S), fwd = bad || top == 0u || !(back > 0.0f) ? 0.0f : __fdividef(1.0f, back);
-    if (bad) back = 0.0f;
+    // values in units of 2^e: exact, and far from both ends of float32
+    const float unit = pow2f(-e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) xh[k] *= unit;
+    const bool none = bad || !(sv > 0.0f);
+    float back = none ? 0.0f : sv, fwd = none ? 0.0f : __frcp_rn(sv);
     uint8_t *sfb = sf + (blk >> 2) * 512 + (blk & 3);
     const bool sf_lane = write && (lane & (LANES - 1)) == 0;
 #pragma unroll 2
@@ -284,9 +296,8 @@ __device__ __forceinline__ void df_parts8(const StageArgs &a, int t, int c0, int
             *reinterpret_cast<uint32_t *>(img + row * 128 + ((((off >> 4) ^ (row & 7)) << 4) | (off & 15))) =
                 bad ? 0u : codes;
         if (sf_lane) sfb[(row >> 7) * C::SFB + (row & 31) * 16 + ((row >> 5) & 3) * 4] = (uint8_t)byte;
-        S = df_next_scale(S);
-        back = bad ? 0.0f : __fmul_rn(sv, S);
-        fwd = fminf(fwd * 6.0f, 3e38f);  // finite: 0 * fwd stays 0
+        back *= 0.125f;
+        fwd *= 8.0f;
     }
 }
 
@@ -372,13 +383,7 @@ __global__ void __launch_bounds__(DS_WARPS * 32) k_fp4_stage(StageArgs a)
         if (mean) eta = (float)(sum / (double)a.K);
     }
     const int e0 = df_exponent<FMT>(top, eta);
-    if (rank == 0 && threadIdx.x == 0) {
-        float S = FMT == AS_FP4_NV ? pow2f(e0) : 1.0f;
-        for (int p = 0; p < a.P; ++p) {
-            a.scale[t * a.P + a.P - 1 - p] = S;
-            S = df_next_scale(S);
-        }
-    }
+    if (rank == 0 && threadIdx.x == 0) a.scale[t] = pow2f(e0);
     if (rank == 0 && threadIdx.x == 0 && a.dpts && !a.mask_in) a.eta[t] = eta;
     for (int kb = kb0 + warp; kb < kb1; kb += warps) {
         const int c0 = 256 * kb + 8 * lane;
@@ -419,10 +424,11 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// A token's P columns times their scales, for every token, to the owner of
-// this lane's output.  (P is a constant so that the columns stay in registers.)
+// The sum of a token's P columns (column P - 1 - p times 8^-p), for every token,
+// to the owner of this lane's output.  (P is a constant so that the columns stay
+// in registers.)
 template <int P>
-__device__ __forceinline__ void df_send(uint32_t acc, bool some, int T, int width, const float *scale, uint32_t to)
+__device__ __forceinline__ void df_send(uint32_t acc, bool some, int T, int width, uint32_t to)
 {
     for (int t0 = 0; t0 < T; t0 += 2) {
         uint32_t r[2][16];  // columns past P, and of a token T, belong to others and are not used
@@ -444,9 +450,9 @@ __device__ __forceinline__ void df_send(uint32_t acc, bool some, int T, int widt
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             if (t0 + u >= T) break;
-            float v = 0.0f;
+            float v = __uint_as_float(r[u][0]);
 #pragma unroll
-            for (int p = 0; p < P; ++p) v = fmaf(__uint_as_float(r[u][p]), scale[(t0 + u) * P + p], v);
+            for (int p = 1; p < P; ++p) v = fmaf(v, 0.125f, __uint_as_float(r[u][p]));
             st_cluster_f32(to + 4u * (uint32_t)((t0 + u) * width), v);
         }
     }
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<FMT, NB>::PER_SM) k_decode_f
     constexpr int S = P::STAGES;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(16) float recv[DF_RECV];
-    __shared__ float s_scale[NB], s_rowf[DF_ROWS], s_rowsum[DF_ROWS], s_eta[16];
+    __shared__ float s_scale[16], s_rowf[DF_ROWS], s_rowsum[DF_ROWS], s_eta[16];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                             ~uintptr_t(1023));
     // every W and X image is 1024-byte aligned
@@ -575,8 +581,10 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<FMT, NB>::PER_SM) k_decode_f
         s_rowf[u] = a.rowf[uo];
         s_rowsum[u] = a.eta && uo < a.n_out ? a.rowsum[uo] : 0.0f;
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the staging kernel's columns and means
-        for (int i = u; i < a.T * a.P; i += 128) s_scale[i] = a.scale[i];
-        if (u < a.T) s_eta[u] = a.eta ? a.eta[u] : 0.0f;
+        if (u < a.T) {
+            s_scale[u] = a.scale[u];
+            s_eta[u] = a.eta ? a.eta[u] : 0.0f;
+        }
         asm volatile("bar.sync 1, 128;" ::: "memory");
         const bool ok = mbar_wait(done, 0);
         tc_fence_after();
@@ -585,8 +593,8 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<FMT, NB>::PER_SM) k_decode_f
         const uint32_t to = mapa_u32(smem_u32(recv + (size_t)rank * a.T * width + o - first_of(owner)), (uint32_t)owner);
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
         const bool some = ok && kb1 > kb0;
-        if (a.P == DF_PARTS_BF16) df_send<DF_PARTS_BF16>(acc, some, a.T, width, s_scale, to);
-        else df_send<DF_PARTS_F32>(acc, some, a.T, width, s_scale, to);
+        if (a.P == DF_PARTS_BF16) df_send<DF_PARTS_BF16>(acc, some, a.T, width, to);
+        else df_send<DF_PARTS_F32>(acc, some, a.T, width, to);
         tc_fence_before();
     }
     __syncwarp();
@@ -600,8 +608,11 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<FMT, NB>::PER_SM) k_decode_f
         if (!as_in((long long)t * a.n_out + o, (long long)a.T * a.n_out)) continue;
         float s = 0.0f;
         for (int r = 0; r < nranks; ++r) s += recv[(r * a.T + t) * width + c];
-        s *= s_rowf[o0 + c];
-        if (a.eta) s = fmaf(s_eta[t], s_rowsum[o0 + c], s);
+        // in double: S, the row factor and the sum may leave float32 while their
+        // product does not
+        double d = (double)s * s_scale[t] * s_rowf[o0 + c];
+        if (a.eta) d += (double)s_eta[t] * s_rowsum[o0 + c];
+        s = (float)d;
         if (a.out_bf16) static_cast<__nv_bfloat16 *>(a.y)[(size_t)t * a.n_out + o] = __float2bfloat16_rn(s);
         else static_cast<float *>(a.y)[(size_t)t * a.n_out + o] = s;
     }
@@ -664,7 +675,7 @@ static int df_parts(bool out_bf16) { return out_bf16 ? DF_PARTS_BF16 : DF_PARTS_
 static int df_cols(int T, int parts) { return (T * parts + 15) / 16 * 16; }
 static size_t df_xbytes(int N, int fmt) { return (size_t)N * 128 + (size_t)((N + 127) / 128) * (fmt == AS_FP4_NV ? 2048 : 1024); }
 
-// keep words, eta, column scales, staged columns (the larger of both formats)
+// keep words, eta, the tokens' S, staged columns (the larger of both formats)
 DecodeFp4Layout decode_fp4_layout(int T, int K, int out_bf16)
 {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -673,7 +684,7 @@ DecodeFp4Layout decode_fp4_layout(int T, int K, int out_bf16)
     DecodeFp4Layout l{};
     l.eta = up((size_t)T * ((K + 31) / 32) * sizeof(uint32_t));
     l.scale = l.eta + up((size_t)T * sizeof(float));
-    l.xq = l.scale + up((size_t)n * sizeof(float));
+    l.xq = l.scale + up((size_t)T * sizeof(float));
     l.bytes = l.xq + up((size_t)df_kblocks(K) * xb);
     return l;
 }

@@ -195,12 +195,12 @@ struct DecodeFp4Args {
     void *y;
     int out_bf16;
     // set by the launcher: parts per value, columns (T * P rounded up), factors
-    // inside Wd, column scales and images in the workspace
+    // inside Wd, the tokens' scales and images in the workspace
     int P, N;
     const float *rowf, *scale;
     const uint8_t *xq;
 };
-// Workspace offsets: keep words at 0, eta, column scales, staged columns.
+// Workspace offsets: keep words at 0, eta, the tokens' scales, staged columns.
 struct DecodeFp4Layout {
     size_t eta, scale, xq, bytes;
 };

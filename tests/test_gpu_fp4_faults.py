@@ -130,3 +130,105 @@ def test_one_sparse_layer_on_two_streams(sl):  # noqa: F811
         ok(sl)
         for w, g in zip(want, got):
             assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
+# ------------------------------------------------- how decode holds x
+def one_hot(K, fmt, code=2, byte=None, w_scale=1.0):
+    """Weights [K, K] whose row o reads channel o only: every output is one
+    value of x times (E2M1 of code) * scale * w_scale."""
+    q = np.zeros((K, K), np.uint8)
+    q[np.arange(K), np.arange(K)] = code
+    b = np.full((K, K // o.BLOCK[fmt]), byte if byte is not None else (127 if fmt == o.MX else 56), np.uint8)
+    return q[:, 0::2] | (q[:, 1::2] << 4), b, np.full(K, w_scale, np.float32)
+
+
+def decode_values(sl, x, fmt, out, w=None, cfg=None):  # noqa: F811
+    """prune(x) as the decode holds it, through one-hot weights."""
+    T, K = x.shape
+    wc, wb, wS = w or one_hot(K, fmt)
+    Wd = torch.empty(sl.as_fp4_decode_bytes(K, K, fmt), dtype=torch.uint8, device="cuda")
+    sl.as_weight_prep_fp4(dev(wc), dev(o.tile_scales(wb, fmt)), Wd, w_scale=dev(wS), fmt=fmt)
+    cfg = cfg or sl.config(sel=sl.AS_SEL_ALL, out_dtype=sl.AS_F32 if out == torch.float32 else sl.AS_BF16)
+    y = torch.empty(T, K, dtype=out, device="cuda")
+    ws = torch.empty(sl.as_workspace_size(sl.AS_OP_DECODE_FP4, T, K, K, cfg), dtype=torch.uint8, device="cuda")
+    sl.as_linear_decode_fp4(x.cuda(), Wd, cfg, y, fmt=fmt, workspace=ws)
+    ok(sl)
+    return f32(y).astype(np.float64)
+
+
+HELD = {torch.bfloat16: 2.0 ** -22, torch.float32: 2.0 ** -28}
+
+
+def check_held(x, y, fmt, out, factor=1.0):
+    """A kept value errs by HELD of its block's largest (NV: or of 2^-17 of its
+    token's largest, if more), by a few float32 roundings of itself (the parts'
+    sum, the factor) and by the output's rounding, which among subnormal numbers
+    is half of 2^-133 (bf16) or of 2^-149."""
+    v = x.double().numpy()
+    top = np.repeat(np.abs(v).reshape(v.shape[0], -1, o.BLOCK[fmt]).max(-1), o.BLOCK[fmt], axis=1)
+    if fmt == o.NV:
+        top = np.maximum(top, 2.0 ** -17 * np.abs(v).max(-1, keepdims=True))
+    half = 2.0 ** -8 if out == torch.bfloat16 else 0.0
+    tol = HELD[out] * top * factor + (3 * 2.0 ** -24 + half) * np.abs(v) * factor
+    tol = tol + (2.0 ** -134 if out == torch.bfloat16 else 2.0 ** -149)
+    err = np.abs(y - v * factor)
+    assert (err <= tol).all(), (float((err / tol).max()), np.argwhere(err > tol)[:4])
+
+
+def held_rows(K, dtype):
+    g = np.random.default_rng(91)
+    rows = [g.laplace(0, 0.3, K)]
+    for big in (1e3, 1e4, 1e6):  # one value of a block of 16 above the others
+        r = g.standard_normal(K)
+        r[g.integers(0, 16, K // 16) + 16 * np.arange(K // 16)] *= big
+        rows.append(r)
+    # values that leave the most after every part: 0.5 of its last place each
+    # time, in either direction, and one part too many for the last
+    for ratio in (6.0, 8.0):
+        for lead, last in ((4.0, 4.999), (2.5, 2.4999), (3.5, 3.4999), (0.25, 0.2499)):
+            v = last
+            for _ in range(9):
+                v = lead + v / ratio
+            rows.append(v * np.exp2(g.integers(-3, 4, K // 16)).repeat(16) * np.where(np.arange(K) % 2, 1.0, -1.0))
+            rows[-1][::16] = 4.0 * np.abs(rows[-1][1::16])
+    rows.append(g.standard_normal(K) * np.exp2(g.integers(-40, 40, K)))
+    return torch.from_numpy(np.array(rows).astype(np.float32)).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", [o.MX, o.NV])
+def test_decode_holds_x(sl, fmt, out, dtype):  # noqa: F811
+    x = held_rows(512, dtype)
+    check_held(x, decode_values(sl, x, fmt, out), fmt, out)
+    for t in (0, 3):  # one token takes another column count
+        check_held(x[t:t + 1], decode_values(sl, x[t:t + 1], fmt, out), fmt, out)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", [o.MX, o.NV])
+def test_decode_tiny_and_huge_tokens(sl, fmt, out):  # noqa: F811
+    """Tokens near both ends of float32, pruned and not.  MX holds a block by a
+    normal power of two, so its sums are exact down to 2^-126 only."""
+    g = np.random.default_rng(92)
+    K = 256
+    base = g.standard_normal((8, K)) * (g.random((8, K)) < 0.7)
+    scale = np.exp2(np.array([-149.0, -140, -127, -120, -100, 100, 120, 125]))[:, None]
+    x = torch.from_numpy((base * scale).clip(-3.4e38, 3.4e38).astype(np.float32))
+    if fmt == o.MX:
+        x[:3] = 0.0
+    check_held(x, decode_values(sl, x, fmt, out), fmt, out)
+    cfg = sl.config(sel=sl.AS_SEL_NM, n=2, m=4, out_dtype=sl.AS_F32)
+    y = decode_values(sl, x, fmt, torch.float32, cfg=cfg)
+    kept = np.where(y != 0, x.double().numpy(), 0.0)
+    assert (np.count_nonzero(y, axis=1) <= K // 2).all()
+    check_held(torch.from_numpy(kept), y, fmt, torch.float32)
+
+
+def test_decode_sums_do_not_overflow_before_the_row_scale(sl):  # noqa: F811
+    """Weights are stored 2688 times their row scale: a large x times them stays
+    finite when the output is."""
+    x = torch.from_numpy((np.random.default_rng(93).uniform(1, 3, (2, 256)) * 1e38).astype(np.float32))
+    w = one_hot(256, o.NV, code=7, byte=126, w_scale=2.0 ** -12)
+    y = decode_values(sl, x, o.NV, torch.float32, w=w)
+    check_held(x, y, o.NV, torch.float32, factor=2688 * 2.0 ** -12)
