@@ -71,21 +71,24 @@ __global__ void __launch_bounds__(256) k_fp4_decode_layout(const uint8_t *__rest
     const int kb = blockIdx.x, mt = blockIdx.y, nkb = gridDim.x, kt = fp4_sf_ktiles(K, FMT);
     uint8_t *unit = Wd + ((size_t)mt * nkb + kb) * df_unit(FMT);
     // MX rows whose largest scale is above 2^8 are stored smaller by a power
-    // of two that their row factor carries: sums of products stay in float32
+    // of two that their row factor carries, so that sums of products stay in
+    // float32; by no more than leaves their smallest scale a scale
     __shared__ int s_shift[DF_ROWS];
     if (threadIdx.x < DF_ROWS) {
         const int o = mt * DF_ROWS + threadIdx.x;
-        uint32_t top = 0;
+        int top = 0, low = 254;
         if (FMT == AS_FP4_MX && o < n_out)
             for (int t = 0; t < kt; ++t) {
                 const uint32_t w = *reinterpret_cast<const uint32_t *>(w_sf + fp4_sf_byte(o, 4 * t, kt));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t b = (w >> (8 * k)) & 0xFFu;
-                    top = max(top, b == 255u ? 0u : b);
+                    const int b = (int)((w >> (8 * k)) & 0xFFu);
+                    if (b == 255 || 4 * t + k >= K / 32) continue;
+                    top = max(top, b);
+                    low = min(low, b);
                 }
             }
-        s_shift[threadIdx.x] = top > 135u ? (int)top - 135 : 0;
+        s_shift[threadIdx.x] = top > 135 ? min(top - 135, low) : 0;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < DF_ROWS * 8; i += 256) {  // 16-byte chunk c of row r
@@ -108,7 +111,7 @@ __global__ void __launch_bounds__(256) k_fp4_decode_layout(const uint8_t *__rest
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int b = (int)((w[k] >> (8 * j)) & 0xFFu);
-                    out |= (uint32_t)(b == 255 ? 255 : max(b - sh, 0)) << (8 * j);
+                    out |= (uint32_t)(b == 255 ? 255 : max(b - sh, 0)) << (8 * j);  // below sh: past K
                 }
                 w[k] = out;
             }

@@ -232,3 +232,25 @@ def test_decode_sums_do_not_overflow_before_the_row_scale(sl):  # noqa: F811
     w = one_hot(256, o.NV, code=7, byte=126, w_scale=2.0 ** -12)
     y = decode_values(sl, x, o.NV, torch.float32, w=w)
     check_held(x, y, o.NV, torch.float32, factor=2688 * 2.0 ** -12)
+
+
+def test_decode_mx_rows_of_far_apart_scales(sl):  # noqa: F811
+    """Rows with block scales up to 2^123 beside blocks of down to 2^-122: every
+    block keeps its own scale, whichever of them x reaches."""
+    K = 512
+    wc, wb, wS = one_hot(K, o.MX)
+    own = np.arange(K) // 32
+    small = np.array([5, 40, 100, 120, 134, 136, 200, 250])[np.arange(K) % 8]
+    wb[np.arange(K), (own + 1) % (K // 32)] = 250   # codes zero there
+    wb[np.arange(K), own] = small
+    x = torch.from_numpy(np.random.default_rng(94).uniform(1, 2, (3, K)).astype(np.float32))
+    y = decode_values(sl, x, o.MX, torch.float32, w=(wc, wb, wS))
+    want = x.double().numpy() * np.exp2(small - 127.0)
+    assert (np.abs(y - want) <= (2.0 ** -27 + 3 * 2.0 ** -24) * np.abs(want)).all()  # block within a factor of 2
+    # and the large blocks beside them
+    q = np.zeros((K, K), np.uint8)
+    q[np.arange(K), (np.arange(K) + 32) % K] = 2
+    x = x * 2.0 ** -100
+    y = decode_values(sl, x, o.MX, torch.float32, w=(q[:, 0::2] | (q[:, 1::2] << 4), wb, wS))
+    want = np.roll(x.double().numpy(), -32, axis=1) * 2.0 ** 123
+    assert (np.abs(y - want) <= (2.0 ** -27 + 3 * 2.0 ** -24) * np.abs(want)).all()
