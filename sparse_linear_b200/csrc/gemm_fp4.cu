@@ -261,7 +261,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
                     tc_fence_after();
                     const int next = stage + 1 == S ? 0 : stage + 1;
                     const uint32_t nphase = stage + 1 == S ? phase ^ 1 : phase;
-                    ready = mbar_try_wait(&full[next], nphase);
+                    // not after the pair's last K block: nothing would fill it
+                    ready = (kb + 1 < p.k_blocks || tile + npairs < num_tiles) && mbar_try_wait(&full[next], nphase);
                     const int steps = min(4, (p.K - kb * C::KB + 63) >> 6);
                     const uint32_t sfa = tmem + PAIR_BN + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
                     const uint64_t a_desc = sdesc_kmajor_sw128(smem_u32(sA + stage * P::A));
