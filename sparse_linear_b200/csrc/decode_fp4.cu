@@ -547,7 +547,9 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<FMT, NB>::PER_SM) k_decode_f
             tc_fence_after();
             const int next = stage + 1 == S ? 0 : stage + 1;
             const uint32_t nphase = stage + 1 == S ? phase ^ 1 : phase;
-            ready = kb + 1 < kb1 && mbar_try_wait(&full[next], nphase);
+            // test_wait: this stage's MMAs are ready and do not wait for the next's
+            // (8 tokens 4096 x 14336: 12.6 us against 13.5 with try_wait)
+            ready = kb + 1 < kb1 && mbar_test(&full[next], nphase);
             const int steps = min(4, (a.K - kb * DF_KB + 63) >> 6);
             const uint32_t sfa = tmem + NB + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
             const unsigned char *x = sX + stage * P::XB;

@@ -252,6 +252,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
             int it = 0;
             // A barrier's answer takes some 240 clocks here even when it is
             // ready: the next stage is asked for before this one's MMAs issue.
+            // (test_wait, which never suspends and then has to ask again:
+            // 777 x 11008 x 4096 22.3 us against 21.5.)
             bool ready = false;
             for (int tile = pair; tile < num_tiles && !*(volatile int *)abort_flag; tile += npairs, ++it) {
                 if (!mbar_wait(acc_empty, (it & 1) ^ 1)) { *(volatile int *)abort_flag = 1; break; }
@@ -580,7 +582,8 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
             tc_fence_after();
             const int next = stage + 1 == S ? 0 : stage + 1;
             const uint32_t nphase = stage + 1 == S ? phase ^ 1 : phase;
-            ready = kb + 1 < kb1 && mbar_try_wait(&full[next], nphase);
+            // test_wait: this stage's MMAs are ready and do not wait for the next's
+            ready = kb + 1 < kb1 && mbar_test(&full[next], nphase);
             const int steps = min(4, (p.K - kb * C::KB + 63) >> 6);
             const uint32_t sfa = tmem + N + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;
 #pragma unroll
