@@ -24,6 +24,7 @@ FLAGS = [
 
 def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+                  + glob.glob(os.path.join(CSRC, "*.h"))
                   + [os.path.join(HERE, "..", "include", "actsparse.h")])
 
 

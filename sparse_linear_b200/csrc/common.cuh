@@ -14,6 +14,7 @@
 #include <stdint.h>
 
 #include "../../include/actsparse.h"
+#include "once.h"
 
 #ifndef AS_SPIN_LIMIT
 #define AS_SPIN_LIMIT (1u << 22)  // ~4M polls: seconds, far beyond any legitimate wait
@@ -394,17 +395,16 @@ __device__ __forceinline__ void tmem_cp_128x128b_pair(uint32_t taddr, uint64_t s
 }
 
 // ------------------------------------------------------------ host helpers
-// Raises a kernel's dynamic shared-memory limit to `smem` once per device
-// (the caller passes a static array of its own, one per kernel instance).
+// Raises a kernel's dynamic shared-memory limit to `smem` (the caller passes a
+// static record of its own, one per kernel instance).
 template <typename Kernel>
-static cudaError_t smem_limit_once(Kernel kernel, size_t smem, int (&done)[64])
+static cudaError_t smem_limit_once(Kernel kernel, size_t smem, RaisedLimit &limit)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-    if (dev >= 0 && dev < 64 && done[dev] >= (int)smem) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = (int)smem;
-    return e;
+    return (cudaError_t)limit.raise(dev, (int)smem, [&](int n) {
+        return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+    });
 }
 
 // -------------------------------------------------------------- misc

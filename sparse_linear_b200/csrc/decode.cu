@@ -1067,7 +1067,7 @@ static cudaError_t launch_tc_one(const DecodeArgs &a, const DecodePlan &p, cudaS
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     set_pdl(cfg, attr);
-    static int done[64];
+    static RaisedLimit done;
     cudaError_t e = smem_limit_once(k_decode_tc<TP, FUSED, LO, DENSE>, smem, done);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k_decode_tc<TP, FUSED, LO, DENSE>, a, p.words_per_split);
     return e;

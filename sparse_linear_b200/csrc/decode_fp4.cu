@@ -647,12 +647,12 @@ template <int FMT, int NB>
 static cudaError_t launch_df(const DecodeFp4Args &a, cudaStream_t st)
 {
     using P = DfCfg<FMT, NB>;
-    static int done[64];
+    static RaisedLimit done;
     const cudaError_t e = smem_limit_once(k_decode_fp4<FMT, NB>, P::smem, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    static int fit[9];
+    static DeviceAnswer fit[9];
     df_launch(cfg, attr, dim3(1), DF_THREADS, P::smem, 1, st);
     const int ranks =
         cluster_that_fits(k_decode_fp4<FMT, NB>, cfg, df_mtiles(a.n_out), P::PER_SM, df_kblocks(a.K), fit);

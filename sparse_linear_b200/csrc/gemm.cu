@@ -847,14 +847,14 @@ static bool make_map_u8(CUtensorMap *m, const void *base, uint64_t rows, uint64_
 
 static int sm_count()
 {
-    static int n = 0;
-    if (!n) {
-        int dev = 0;
-        cudaGetDevice(&dev);
+    static DeviceAnswer known;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    return known.get(dev, [&] {
+        int n = 0;
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (n <= 0) n = 148;
-    }
-    return n;
+        return n > 0 ? n : 148;
+    });
 }
 
 template <bool SPARSE>
@@ -899,45 +899,47 @@ static cudaError_t launch_gemm_t(const GemmArgs &a, cudaStream_t st)
 // Number of 2-CTA clusters of k_gemm_sp_pair that fit on the device at once
 // (0 if the query fails).
 template <typename KernelT>
-static int pair_clusters_of(KernelT kernel, size_t smem, int &cached, int threads = PAIR_THREADS)
+static int pair_clusters_of(KernelT kernel, size_t smem, DeviceAnswer &cached, int threads = PAIR_THREADS)
 {
-    if (cached >= 0) return cached;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * 74, 1, 1);
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        n = 0;
-    }
-    cached = n;
-    return n;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    return cached.get(dev, [&] {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(2 * 74, 1, 1);
+        cfg.blockDim = dim3(threads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        return n;
+    });
 }
 
 static int pair_clusters(size_t smem)
 {
-    static int cached = -1;
+    static DeviceAnswer cached;
     return pair_clusters_of(k_gemm_sp_pair<false>, smem, cached);
 }
 
 static int pair_clusters_fp8(size_t smem)
 {
-    static int cached = -1;
+    static DeviceAnswer cached;
     return pair_clusters_of(k_gemm_sp_pair<true>, smem, cached);
 }
 
 static int dense_pair_clusters(size_t smem)
 {
-    static int cached = -1;
+    static DeviceAnswer cached;
     return pair_clusters_of(k_gemm_dense_pair, smem, cached);
 }
 

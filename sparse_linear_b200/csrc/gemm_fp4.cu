@@ -703,10 +703,10 @@ static cudaError_t launch_fp4_pair(const Fp4GemmArgs &a, cudaStream_t st)
         !make_map_sf(&mSA, a.x_sf, (uint64_t)((a.T + 127) / 128) * p.kt, Fp4Cfg<FMT>::SFT) ||
         !make_map_sf(&mSB, a.w_sf, (uint64_t)((a.n_out + 127) / 128) * p.kt, Fp4Cfg<FMT>::SFT))
         return cudaErrorInvalidValue;
-    static int cached = -1;
+    static DeviceAnswer cached;
     const int clusters = pair_clusters_of(k_gemm_fp4_pair<FMT>, FpPair<FMT>::smem, cached, FP_THREADS);
     if (clusters <= 0) return cudaErrorNotSupported;
-    static int done[64];
+    static RaisedLimit done;
     cudaError_t e = smem_limit_once(k_gemm_fp4_pair<FMT>, FpPair<FMT>::smem, done);
     if (e != cudaSuccess) return e;
     const int grid = 2 * std::min(p.m_tiles * p.n_tiles, clusters);
@@ -718,18 +718,19 @@ static cudaError_t launch_fp4_pair(const Fp4GemmArgs &a, cudaStream_t st)
 // block) with which the clusters of all tiles are resident at once.  CTAs that
 // the SMs hold / tiles is not that: a cluster stays within one GPC, so that 16
 // clusters of 8 need two waves on 148 SMs (256 x 1024 x 4096: 18.8 us so, 10.7
-// with the most that fit).  fit[r] keeps the device's answer for r, plus one.
+// with the most that fit).  fit[r] keeps each device's answer for r.
 // With two CTAs per SM the SMs' count decides: the answer counts one per SM,
 // and a cluster that is left over shares SMs (decode, one token, 11008 x 14336:
 // 19.7 us so, 26.9 by the answer).
 template <typename Kernel>
-static int cluster_that_fits(Kernel kernel, cudaLaunchConfig_t cfg, int tiles, int per_sm, int k_blocks, int (&fit)[9])
+static int cluster_that_fits(Kernel kernel, cudaLaunchConfig_t cfg, int tiles, int per_sm, int k_blocks, DeviceAnswer (&fit)[9])
 {
-    int r = std::max(1, std::min(8, k_blocks));
+    int r = std::max(1, std::min(8, k_blocks)), dev = 0;
+    cudaGetDevice(&dev);
     for (; r > 1; --r) {
         if (tiles > per_sm * sm_count() / r) continue;
         if (per_sm > 1) break;
-        if (!fit[r]) {
+        const int clusters = fit[r].get(dev, [&] {
             cudaLaunchAttribute at{};
             at.id = cudaLaunchAttributeClusterDimension;
             at.val.clusterDim.x = r;
@@ -742,9 +743,9 @@ static int cluster_that_fits(Kernel kernel, cudaLaunchConfig_t cfg, int tiles, i
                 cudaGetLastError();
                 n = 0;
             }
-            fit[r] = n + 1;
-        }
-        if (tiles < fit[r]) break;
+            return n;
+        });
+        if (tiles <= clusters) break;
     }
     return r;
 }
@@ -762,7 +763,7 @@ static cudaError_t launch_fp4_few(const Fp4GemmArgs &a, cudaStream_t st)
         !make_map_sf(&mSA, a.w_sf, (uint64_t)p.m_tiles * p.kt, Fp4Cfg<FMT>::SFT) ||
         !make_map_sf(&mSB, a.x_sf, (uint64_t)((a.T + 127) / 128) * p.kt, Fp4Cfg<FMT>::SFT))
         return cudaErrorInvalidValue;
-    static int done[64];
+    static RaisedLimit done;
     cudaError_t e = smem_limit_once(k_gemm_fp4_few<FMT, N>, P::smem, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -775,7 +776,7 @@ static cudaError_t launch_fp4_few(const Fp4GemmArgs &a, cudaStream_t st)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    static int fit[9];
+    static DeviceAnswer fit[9];
     const int ranks = cluster_that_fits(k_gemm_fp4_few<FMT, N>, cfg, p.m_tiles * p.n_tiles, 1, p.k_blocks, fit);
     cfg.gridDim = dim3(ranks, p.m_tiles, p.n_tiles);
     attr[0].val.clusterDim.x = ranks;

@@ -323,7 +323,7 @@ static cudaError_t launch_norm_ring(const NormArgs &a, int T, int D, cudaStream_
     const size_t room = (PER_SM == 3 ? 72 : 220) * 1024 - (size_t)kt * 4;
     const int stages = (int)std::min<size_t>(NR_STAGES, room / row);
     const size_t smem = stages * row + (size_t)kt * 4;
-    static int done[64];
+    static RaisedLimit done;
     const cudaError_t e = smem_limit_once(k_norm_ring<NT, CH, PER_SM>, smem, done);
     if (e != cudaSuccess) return e;
     k_norm_ring<NT, CH, PER_SM><<<PER_SM * sm_count(), NT, smem, st>>>(a, T, D, kt, stages);

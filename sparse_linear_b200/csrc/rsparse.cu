@@ -165,7 +165,7 @@ static cudaError_t launch_rs_t(const RsparseArgs &a, cudaStream_t st)
     float *part = static_cast<float *>(a.workspace);
     const size_t red = (size_t)RS_WARPS * TP * 32 * RL * sizeof(float);
     if (red > 48 * 1024) {
-        static int done[64];
+        static RaisedLimit done;
         const cudaError_t e = smem_limit_once(k_rs_u<TW, TP, RL>, red, done);
         if (e != cudaSuccess) return e;
     }

@@ -201,12 +201,12 @@ cudaError_t launch_rsp_u(const void *x, const uint32_t *mask, const float *eta, 
     const size_t smem = (size_t)4 * RSP_TM * RSP_XP * 2 + (size_t)2 * RSP_KB * (r + 8) * 2;
     cudaError_t e;
     if (r == 64) {
-        static int done[64];
+        static RaisedLimit done;
         e = smem_limit_once(k_rsp_u<64>, smem, done);
         if (e == cudaSuccess)
             k_rsp_u<64><<<grid, RSP_THREADS, smem, st>>>(xb, mask, eta, Bb, T, K, L.blocks_per_split, part);
     } else {
-        static int done[64];
+        static RaisedLimit done;
         e = smem_limit_once(k_rsp_u<128>, smem, done);
         if (e == cudaSuccess)
             k_rsp_u<128><<<grid, RSP_THREADS, smem, st>>>(xb, mask, eta, Bb, T, K, L.blocks_per_split, part);

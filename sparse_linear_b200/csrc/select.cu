@@ -792,14 +792,14 @@ cudaError_t launch_colnorm(const void *x, int bf16, int T, int K, float *c, void
     cudaError_t e;
     if (bf16) {
         const size_t smem = (size_t)CN_BUFS_BF16 * CN_WIN * 2;
-        static int done[64];
+        static RaisedLimit done;
         e = smem_limit_once(k_colsq_ring<__nv_bfloat16, CN_BUFS_BF16>, smem, done);
         if (e == cudaSuccess)
             k_colsq_ring<__nv_bfloat16, CN_BUFS_BF16><<<grid, CN_THREADS, smem, st>>>(
                 static_cast<const __nv_bfloat16 *>(x), T, K, part);
     } else {
         const size_t smem = (size_t)CN_BUFS_F32 * CN_WIN * 4;
-        static int done[64];
+        static RaisedLimit done;
         e = smem_limit_once(k_colsq_ring<float, CN_BUFS_F32>, smem, done);
         if (e == cudaSuccess)
             k_colsq_ring<float, CN_BUFS_F32><<<grid, CN_THREADS, smem, st>>>(static_cast<const float *>(x), T, K, part);
@@ -814,7 +814,7 @@ template <typename TX, int NT>
 static cudaError_t launch_select_t(const SelectArgs &a, size_t smem, int grid, cudaStream_t st)
 {
     if (smem > 40 * 1024) {  // the 48 KB default also counts the kernel's static shared memory
-        static int done[64];
+        static RaisedLimit done;
         cudaError_t e = smem_limit_once(k_select<TX, NT>, smem, done);
         if (e != cudaSuccess) return e;
     }
@@ -837,7 +837,7 @@ template <typename TX, int M, bool COMPACT, bool FREG>
 static cudaError_t launch_select_rows_f(const SelectArgs &a, cudaStream_t st)
 {
     const size_t smem = ((a.f && !FREG) ? (size_t)a.K * 4 : 0) + (size_t)SR_BUFS * a.K * sizeof(TX);
-    static int done[64];
+    static RaisedLimit done;
     cudaError_t e = smem_limit_once(k_select_rows<TX, M, COMPACT, FREG>, smem, done);
     if (e != cudaSuccess) return e;
     int per_sm = 0, dev = 0, sms = 0;

@@ -254,3 +254,48 @@ def test_decode_mx_rows_of_far_apart_scales(sl):  # noqa: F811
     y = decode_values(sl, x, o.MX, torch.float32, w=(q[:, 0::2] | (q[:, 1::2] << 4), wb, wS))
     want = np.roll(x.double().numpy(), -32, axis=1) * 2.0 ** 123
     assert (np.abs(y - want) <= (2.0 ** -27 + 3 * 2.0 ** -24) * np.abs(want)).all()
+
+
+def test_norm_step_from_many_threads(sl):  # noqa: F811
+    """Calls of one kernel that need different shared memory, from host threads
+    that start together (a new process would meet them as its first calls)."""
+    import threading
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cases = []
+    for i, (D, rdt, ydt) in enumerate([(2056, torch.bfloat16, torch.bfloat16), (4096, torch.float32, torch.float32),
+                                       (2080, torch.bfloat16, torch.float32), (4096, torch.float32, torch.bfloat16)]):
+        r = torch.randn(600, D, generator=g, device="cuda").to(rdt)
+        y = torch.randn(600, D, generator=g, device="cuda").to(ydt)
+        gate = torch.randn(600, D, generator=g, device="cuda") if i % 2 else None
+        cases.append((r, y, gate))
+    got, errors = [None] * 8, []
+    gate_open = threading.Barrier(8)
+    streams = [torch.cuda.Stream() for _ in range(8)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        r, y, gate = cases[i % 4]
+        try:
+            with torch.cuda.stream(streams[i]):
+                out = torch.empty_like(r)
+                h = torch.empty(r.shape, device="cuda")
+                gate_open.wait(30)
+                for _ in range(20):
+                    sl.as_norm_residual(r, y=y, r_out=out, h=h, gate=gate, post_norm=True)
+            got[i] = (out, h)
+        except Exception as e:  # noqa: BLE001 (reported below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    ok(sl)
+    assert not errors, errors
+    for i in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(got[i], got[i + 4]))
+        n = lambda v: None if v is None else v.double().cpu().numpy()  # noqa: E731
+        r, y, gate = cases[i]
+        _, h = o.norm_residual(n(r), n(y), True, None, n(gate))
+        assert np.abs(f32(got[i][1]) - h).max() <= 1e-4  # |h| < 8: its roundings are below 40 * 2^-24 * 8 = 2e-5
