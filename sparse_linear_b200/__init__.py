@@ -416,6 +416,7 @@ def as_linear_prefill_nm_split(sel: as_select_out, T: int, W, cfg: as_config, y,
 # ------------------------------------------- microscaled 4-bit, norm step
 # These calls are a few microseconds on the GPU, so their checks are too: one
 # pass over each tensor, sizes computed here rather than through the library.
+_SIZES = 1024  # sizes remembered; a server sees any number of prompt lengths
 _U8, _F32, _BF16, _I32 = torch.uint8, torch.float32, torch.bfloat16, torch.int32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # of a device index
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # a device tensor exists by then
@@ -468,7 +469,7 @@ def _workspace_bytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=_SIZES)
 def as_fp4_sf_bytes(rows: int, K: int, fmt: int = AS_FP4_NV) -> int:
     """Bytes of the scale buffer of rows x K microscaled values."""
     n = _lib.as_fp4_sf_bytes(int(rows), int(K), int(fmt))
@@ -477,7 +478,7 @@ def as_fp4_sf_bytes(rows: int, K: int, fmt: int = AS_FP4_NV) -> int:
     return n
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=_SIZES)
 def as_fp4_decode_bytes(n_out: int, K: int, fmt: int = AS_FP4_NV) -> int:
     """Bytes of the decode layout of a quantised weight [n_out, K]."""
     n = _lib.as_fp4_decode_bytes(int(n_out), int(K), int(fmt))

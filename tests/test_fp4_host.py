@@ -126,6 +126,14 @@ def test_sizes(lib):
         lib.as_workspace_size(lib.AS_OP_DECODE_FP4, 17, 4096, 64, cfg)
 
 
+def test_sizes_of_any_number_of_lengths(lib):
+    """What the size queries remember stays bounded."""
+    for f in (lib.as_fp4_sf_bytes, lib.as_fp4_decode_bytes):
+        for rows in range(8, 8 * 3000, 8):
+            f(rows, 64, lib.AS_FP4_NV)
+        assert f.cache_info().currsize <= 2000
+
+
 def test_quant_refusals(lib):
     f = lib._lib.as_quant_fp4
 
