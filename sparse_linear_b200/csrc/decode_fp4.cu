@@ -70,6 +70,8 @@ __global__ void __launch_bounds__(256) k_fp4_decode_layout(const uint8_t *__rest
     using C = Fp4Cfg<FMT>;
     const int kb = blockIdx.x, mt = blockIdx.y, nkb = gridDim.x, kt = fp4_sf_ktiles(K, FMT);
     uint8_t *unit = Wd + ((size_t)mt * nkb + kb) * df_unit(FMT);
+    // every write below is at a constant bound inside the unit
+    if (!as_in(kb, (K + DF_KB - 1) / DF_KB) || !as_in((long long)mt * DF_ROWS, n_out)) return;
     // MX rows whose largest scale is above 2^8 are stored smaller by a power
     // of two that their row factor carries, so that sums of products stay in
     // float32; by no more than leaves their smallest scale a scale
@@ -295,10 +297,10 @@ __device__ __forceinline__ void df_parts8(const StageArgs &a, int t, int c0, int
             xh[2 * k + 1] = fmaf(-q.y, back, xh[2 * k + 1]);
         }
         const int row = t * a.P + a.P - 1 - p;
-        if (write)
-            *reinterpret_cast<uint32_t *>(img + row * 128 + ((((off >> 4) ^ (row & 7)) << 4) | (off & 15))) =
-                bad ? 0u : codes;
-        if (sf_lane) sfb[(row >> 7) * C::SFB + (row & 31) * 16 + ((row >> 5) & 3) * 4] = (uint8_t)byte;
+        uint8_t *code_at = img + row * 128 + ((((off >> 4) ^ (row & 7)) << 4) | (off & 15));
+        uint8_t *sf_at = sfb + (row >> 7) * C::SFB + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+        if (write && as_in(code_at + 3 - img, a.N * 128)) *reinterpret_cast<uint32_t *>(code_at) = bad ? 0u : codes;
+        if (sf_lane && as_in(sf_at - sf, (long long)a.xb - a.N * 128)) *sf_at = (uint8_t)byte;
         back *= 0.125f;
         fwd *= 8.0f;
     }
@@ -386,13 +388,16 @@ __global__ void __launch_bounds__(DS_WARPS * 32) k_fp4_stage(StageArgs a)
         if (mean) eta = (float)(sum / (double)a.K);
     }
     const int e0 = df_exponent<FMT>(top, eta);
-    if (rank == 0 && threadIdx.x == 0) a.scale[t] = pow2f(e0);
-    if (rank == 0 && threadIdx.x == 0 && a.dpts && !a.mask_in) a.eta[t] = eta;
+    if (rank == 0 && threadIdx.x == 0 && as_in(t, a.T)) {
+        a.scale[t] = pow2f(e0);
+        if (a.dpts && !a.mask_in) a.eta[t] = eta;
+    }
     for (int kb = kb0 + warp; kb < kb1; kb += warps) {
         const int c0 = 256 * kb + 8 * lane;
         float xh[8];
         if (kb != kb0 + warp) df_load_raw(a, t, c0, c0 < a.K, raw);
         df_keep8(a, raw, t, c0, c0 < a.K, eta, xh);
+        if (!as_in(kb, nkb)) break;  // the whole warp: images of nkb K blocks
         uint8_t *img = a.xq + (size_t)kb * a.xb;
         df_parts8<FMT>(a, t, c0, e0, xh, img, img + (size_t)a.N * 128);
     }

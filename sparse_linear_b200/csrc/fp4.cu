@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(ROWS *TPR, 1024 / (ROWS * TPR))
         inv_row = pow2f(-e);
         if (i == 0 && row_ok && as_in(row, rows)) row_scale[row] = pow2f(e);
     } else {
-        if (i == 0 && row_ok && row_scale) row_scale[row] = 1.0f;
+        if (i == 0 && row_ok && row_scale && as_in(row, rows)) row_scale[row] = 1.0f;
         __syncthreads();  // the zeroed scales, before they are written
     }
 

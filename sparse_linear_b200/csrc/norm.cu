@@ -57,6 +57,14 @@ __device__ __forceinline__ float block_sum(float v, float *red)
     return v;
 }
 
+// Four scale bytes of row t (up to the next multiple of 128 past T), tile i of kt.
+__device__ __forceinline__ void norm_store_sf(const NormArgs &a, int t, int T, int i, int kt, uint32_t bytes)
+{
+    const size_t at = fp4_sf_byte(t, 4 * i, kt);
+    if (as_in((long long)at + 3, (long long)((T + 127) / 128) * kt * 512))
+        *reinterpret_cast<uint32_t *>(a.h_sf + at) = bytes;
+}
+
 // h -> codes and scales of row t (all threads of the block).
 template <int NT, int CH, int FMT>
 __device__ __forceinline__ void norm_store_fp4(const NormArgs &a, const float (&h)[CH][8], int t, int T, int D, int kt,
@@ -83,7 +91,7 @@ __device__ __forceinline__ void norm_store_fp4(const NormArgs &a, const float (&
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) top = max(top, s_max[w]);
     const int e = FMT == AS_FP4_NV ? nv_row_exponent(top) : 0;
-    if (tid == 0 && a.h_scale) a.h_scale[t] = pow2f(e);
+    if (tid == 0 && a.h_scale && as_in(t, T)) a.h_scale[t] = pow2f(e);
     const float inv_row = pow2f(-e);
 #pragma unroll
     for (int r = 0; r < CH; ++r) {
@@ -96,8 +104,7 @@ __device__ __forceinline__ void norm_store_fp4(const NormArgs &a, const float (&
         if (c % LANES == 0) s_sf[c / LANES] = (unsigned char)b.byte;
     }
     __syncthreads();
-    for (int i = tid; i < kt; i += NT)
-        *reinterpret_cast<uint32_t *>(a.h_sf + fp4_sf_byte(t, 4 * i, kt)) = reinterpret_cast<const uint32_t *>(s_sf)[i];
+    for (int i = tid; i < kt; i += NT) norm_store_sf(a, t, T, i, kt, reinterpret_cast<const uint32_t *>(s_sf)[i]);
 }
 
 template <int NT, int CH>
@@ -108,8 +115,7 @@ __global__ void __launch_bounds__(NT, NT * CH <= 1024 ? 1024 / NT : 1) k_norm_re
     extern __shared__ __align__(16) unsigned char s_sf[];
     const int t = blockIdx.x, tid = threadIdx.x, nch = D >> 3;
     if (t >= T) {  // padding rows of the last 128-row scale tile
-        for (int i = tid; i < kt; i += NT)
-            *reinterpret_cast<uint32_t *>(a.h_sf + fp4_sf_byte(t, 4 * i, kt)) = 0u;
+        for (int i = tid; i < kt; i += NT) norm_store_sf(a, t, T, i, kt, 0u);
         return;
     }
     const size_t row = (size_t)t * D;
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(NT, PER_SM) k_norm_ring(NormArgs a, int T, int
     }
     if (a.h_q)  // padding rows of the last 128-row scale tile
         for (int t = T + blockIdx.x; t < (T + 127) / 128 * 128; t += gridDim.x)
-            for (int i = tid; i < kt; i += NT) *reinterpret_cast<uint32_t *>(a.h_sf + fp4_sf_byte(t, 4 * i, kt)) = 0u;
+            for (int i = tid; i < kt; i += NT) norm_store_sf(a, t, T, i, kt, 0u);
 }
 
 template <int NT, int CH, int PER_SM>
