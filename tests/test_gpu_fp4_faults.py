@@ -208,15 +208,12 @@ def test_decode_holds_x(sl, fmt, out, dtype):  # noqa: F811
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("fmt", [o.MX, o.NV])
 def test_decode_tiny_and_huge_tokens(sl, fmt, out):  # noqa: F811
-    """Tokens near both ends of float32, pruned and not.  MX holds a block by a
-    normal power of two, so its sums are exact down to 2^-126 only."""
+    """Tokens near both ends of float32, pruned and not."""
     g = np.random.default_rng(92)
     K = 256
     base = g.standard_normal((8, K)) * (g.random((8, K)) < 0.7)
     scale = np.exp2(np.array([-149.0, -140, -127, -120, -100, 100, 120, 125]))[:, None]
     x = torch.from_numpy((base * scale).clip(-3.4e38, 3.4e38).astype(np.float32))
-    if fmt == o.MX:
-        x[:3] = 0.0
     check_held(x, decode_values(sl, x, fmt, out), fmt, out)
     cfg = sl.config(sel=sl.AS_SEL_NM, n=2, m=4, out_dtype=sl.AS_F32)
     y = decode_values(sl, x, fmt, torch.float32, cfg=cfg)

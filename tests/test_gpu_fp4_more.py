@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import synth
-from gpu_util import f32
+from gpu_util import f32, unpack_bitmask
 from oracle import fp4 as o
 from test_gpu_fp4 import (Guarded, check_decode, check_norm, check_product, decode_case, dev, ok, prep,  # noqa: F401
                           quantise, random_operand, rng, sl)
@@ -120,6 +120,44 @@ def test_decode_outlier_channels_that_no_weight_reads(sl, fmt, out):  # noqa: F8
     assert (np.abs(f32(y) - ref) <= tol).all()
 
 
+@pytest.mark.parametrize("T,dpts", [(1, 0), (5, 1), (16, 1)])
+def test_decode_then_rsparse(sl, T, dpts):  # noqa: F811
+    """The compensation of the dropped channels behind a 4-bit decode, by the call's
+    own mask and means, without a wait between the two."""
+    K, n_out, r = 1056, 264, 64
+    x, wc, wb, wS = decode_case(11, T, K, n_out, o.NV, torch.bfloat16)
+    g = rng(12, T)
+    B = torch.from_numpy(g.standard_normal((K, r)).astype(np.float32) * 0.1).bfloat16()
+    A = torch.from_numpy(g.standard_normal((n_out, r)).astype(np.float32) * 0.1).bfloat16()
+    w = o.values(wc, wb, wS, o.NV)
+    rowsum = w.sum(1).astype(np.float32)
+    Wd = prep(sl, wc, wb, wS, o.NV)
+    cfg = sl.config(sel=sl.AS_SEL_NM, n=8, m=16, dpts=dpts, out_dtype=sl.AS_F32)
+    ws = torch.empty(sl.as_workspace_size(sl.AS_OP_DECODE_FP4, T, K, n_out, cfg), dtype=torch.uint8, device="cuda")
+    wr = torch.empty(sl.as_rsparse_workspace(T, K, r), dtype=torch.uint8, device="cuda")
+    xd, Bd, Ad, rs = x.cuda(), B.cuda(), A.cuda(), dev(rowsum)
+    outs = []
+    for _ in range(4):
+        y = torch.empty(T, n_out, device="cuda")
+        mask = torch.zeros(T, K // 32, dtype=torch.int32, device="cuda")
+        eta = torch.zeros(T, device="cuda")
+        sl.as_linear_decode_fp4(xd, Wd, cfg, y, fmt=o.NV, rowsum=rs, mask_out=mask, eta_out=eta, workspace=ws)
+        sl.as_rsparse_decode(xd, mask, Bd, Ad, y, eta=eta if dpts else None, workspace=wr)
+        outs.append((y, mask, eta))
+    ok(sl)
+    y, mask, eta = outs[0]
+    assert all(torch.equal(y, other[0]) for other in outs)
+    xf = x.float().numpy()
+    m = unpack_bitmask(mask, K)
+    e = f32(eta)[:, None] if dpts else np.zeros((T, 1), np.float32)
+    xh = (xf - e).astype(np.float32).astype(np.float64)
+    Bf, Af = B.double().numpy(), A.double().numpy()
+    ref = (xh * m) @ w.T + e.astype(np.float64) * rowsum + ((xh * (m == 0)) @ Bf) @ Af.T
+    mag = np.abs(xh) @ np.abs(w).T + np.abs(e * rowsum) + (np.abs(xh) @ np.abs(Bf)) @ np.abs(Af).T
+    # the decode's bound, and sums of up to 16 + K / 128 + r float32 steps in the two factors' products
+    assert (np.abs(f32(y) - ref) <= ((3 * K / 16 / 64 + 27) + 16 + K / 128 + r) * 2.0 ** -22 * mag).all()
+
+
 # ------------------------------------------------------------------ product
 @pytest.mark.parametrize("fmt", [o.MX, o.NV])
 @pytest.mark.parametrize("T,K,n_out", [(1, 288, 20008), (30, 544, 20008), (64, 1056, 38000)])
@@ -146,6 +184,23 @@ def test_quantise_and_multiply_non_finite_rows(sl, T, fmt):  # noqa: F811
     want = np.zeros((T, n_out), bool)
     want[1], want[:, 9] = True, True
     np.testing.assert_array_equal(np.isnan(f32(y.t)), want)
+
+
+@pytest.mark.parametrize("T", [3, 200, 1300])
+@pytest.mark.parametrize("xb,wb", [(0, 254), (254, 0), (1, 253), (0, 120), (50, 57), (254, 100)])
+def test_product_extreme_mx_scales(sl, T, xb, wb):  # noqa: F811
+    """E8M0 scales of 2^-127 and 2^127, sums among the subnormal numbers: the
+    products of 64 channels are whole multiples of 2^(xb + wb - 256), at most 2^14
+    of them, and exact."""
+    K, n_out = 64, 2056
+    xc, xbytes, _, _ = random_operand(31, T, K, o.MX, False)
+    wc, wbytes, _, _ = random_operand(32, n_out, K, o.MX, False)
+    xbytes[:], wbytes[:] = xb, wb
+    y = torch.empty(T, n_out, device="cuda")
+    sl.as_linear_prefill_fp4(dev(xc), dev(o.tile_scales(xbytes, o.MX)), dev(wc), dev(o.tile_scales(wbytes, o.MX)), y,
+                             fmt=o.MX)
+    ok(sl)
+    np.testing.assert_array_equal(f32(y), o.values(xc, xbytes, None, o.MX) @ o.values(wc, wbytes, None, o.MX).T)
 
 
 # ------------------------------------------------------------------ norm
