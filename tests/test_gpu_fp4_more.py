@@ -325,3 +325,58 @@ def test_repeated_runs_give_the_same_bits(sl):  # noqa: F811
         sl.as_linear_prefill_fp4(hq, hsf, wq, wsf, p, x_scale=hs, w_scale=wS, fmt=fmt)
     ok(sl)
     assert all(torch.equal(p, ps[0]) for p in ps)
+
+
+# ------------------------------------------------------------------ first calls
+FIRST_CALLS = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import sparse_linear_b200 as sl
+from sparse_linear_b200.layer import Fp4Linear, SparseLinear
+g = torch.Generator(device="cuda").manual_seed(0)
+W = torch.randn(1032, 2048, generator=g, device="cuda") * 0.02
+x = torch.randn(300, 2048, generator=g, device="cuda").bfloat16()
+r = torch.randn(600, 4096, generator=g, device="cuda")
+y = torch.randn(600, 4096, generator=g, device="cuda")
+cfg = sl.config(score=sl.AS_SCORE_CLACT, sel=sl.AS_SEL_NM, n=8, m=16, out_dtype=sl.AS_F32)
+L, S = Fp4Linear(W, cfg), SparseLinear(W.bfloat16(), cfg)
+
+
+def calls():
+    h, o = torch.empty_like(r), torch.empty_like(r)
+    sl.as_norm_residual(r, y=y, r_out=o, h=h, post_norm=True)
+    return [L.decode(x[:1]), L.decode(x[:16]), L.prefill(x[:20]), L.prefill(x), S.decode(x[:2]), S.prefill(x)[0], h, o]
+
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = calls()
+eager = calls()  # before the graph has run
+torch.cuda.synchronize()
+for _ in range(2):
+    graph.replay()
+    torch.cuda.synchronize()
+    assert sl.as_stream_status() == sl.AS_OK
+    for i, (a, b) in enumerate(zip(captured, eager)):
+        assert torch.equal(a, b), i
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    """A graph captured by a process that has called nothing before, then the same
+    calls outside it, then its replays."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0, out.stdout + out.stderr
+
+
+@pytest.mark.parametrize("fmt", [o.MX, o.NV])
+def test_decode_longest_rows(sl, fmt):  # noqa: F811
+    x, *w = decode_case(9, 2, 131072, 136, fmt, torch.bfloat16)
+    check_decode(sl, x, *w, fmt, sl.config(sel=sl.AS_SEL_NM, n=8, m=16, dpts=True, out_dtype=sl.AS_F32))
