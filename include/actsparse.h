@@ -569,7 +569,9 @@ as_status as_dequant_fp4(const uint8_t *codes, const uint8_t *sf, const float *r
  * weights, both in `fmt`; x_scale [T] and w_scale [n_out] may be NULL (1).
  * Any T >= 1: few tokens stream the weights with K split over a cluster,
  * long prompts run 256 x 256 tiles on CTA pairs.  n_out % 8 == 0.
- * Float32 accumulation in a fixed order (deterministic). */
+ * Float32 accumulation in a fixed order (deterministic).  The order depends on
+ * T, K and n_out (tiles, the split of K): a row's last bits may differ between
+ * calls with other numbers of rows. */
 as_status as_linear_prefill_fp4(const uint8_t *xq, const uint8_t *x_sf, const float *x_scale, int T, int K, int n_out,
                                 const uint8_t *Wq, const uint8_t *w_sf, const float *w_scale, as_fp4 fmt,
                                 as_dtype out_dtype, void *y, cudaStream_t stream);
@@ -595,6 +597,9 @@ as_status as_weight_prep_fp4(const uint8_t *Wq, const uint8_t *w_sf, const float
  * fewer bits than that one.  g and
  * rowsum describe the same W (as_weight_prep on its values).  A non-finite
  * kept value or weight scale makes the outputs that read it NaN.
+ * Sums over the channels are float32, of x times code times block scale; w_scale
+ * and the shift are applied to them in double and rounded once.  Deterministic;
+ * the order of the sums depends on T's column count, K and n_out.
  *   x [T, K] in `dt`; K % 32 == 0, n_out % 8 == 0; cfg->var is not supported.
  *   Workspace: as_workspace_size(AS_OP_DECODE_FP4, T, K, n_out, cfg); no
  *   zero-fill needed, left in an unspecified state. */
@@ -611,7 +616,9 @@ as_status as_linear_decode_fp4(const void *x, as_dtype dt, int T, int K, int n_o
  *   r'_t = res_scale * r_t + gate * u_t           (r_out, rounded to r_dtype)
  *   h_t  = r'_t * rsqrt(mean(r'_t^2) + eps) * (w_offset + pre_w)
  * h uses the float32 r', before it is rounded for storage.  All arithmetic is
- * float32; the mean squares are sums of per-thread partials in a fixed order.
+ * float32; the mean squares are sums of per-thread partials in a fixed order,
+ * which depends on T and D (a row's last bits may differ between calls with
+ * other numbers of rows).
  * With y == NULL only h = norm(r) is formed (r_out, gate, post_w NULL,
  * post_norm 0; res_scale is not used).
  *   r [T, D], y [T, D], h [T, D] each in its own dtype; post_w, pre_w [D]

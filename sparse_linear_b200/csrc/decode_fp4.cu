@@ -30,12 +30,13 @@
 // selection kernel,) k_fp4_stage, which makes the selection and the parts,
 // and k_decode_fp4, whose weight copies start before the parts are ready.  (One
 // kernel, every CTA making the parts of its own channels, took 15.0 us against
-// 10.7 us for one token at 11008 x 4096: the row's mean and the parts are then
-// computed 32 times over, beside the weight stream.)  Calls one after another,
-// bf16 with 8:16, cold weights: 11008 x 4096, one token with the token shift,
-// 12.0 us (25 MB: 2.1 TB/s); 14336 x 4096, 16 tokens, 13.2 us; 14336 x 11008,
-// one token, 19.7 us (89 MB: 4.5 TB/s).  What is not weight stream is the
-// staging (about 5 us), the first loads' latency and the exchange.
+// 10.7 us of both in a set-up of its own: the row's mean and the parts are then
+// computed 32 times over, beside the weight stream.)
+//   Calls one after another in a graph over weights of 400 MB, bf16 with 8:16:
+// 11008 x 4096 NV, one token, 9.9 us (25 MB: 2.5 TB/s), with the token shift
+// 10.3 us; 14336 x 4096 MX, 16 tokens, 12.3 us (float32 output 13.5); 14336 x
+// 11008 NV, one token, 19.1 us (89 MB: 4.6 TB/s).  What is not weight stream is
+// the staging (about 5 us), the first loads' latency and the exchange.
 #include "common.cuh"
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -417,7 +418,8 @@ struct DfCfg {
     static constexpr int XB = NB * 128 + NSB * Fp4Cfg<FMT>::SFB;
     static constexpr int SCOLS = 4 * (1 + NSB) * Fp4Cfg<FMT>::SFT;
     // up to 64 columns two CTAs fit an SM, of one call or of two in a row
-    // (one token 12.0 us against 13.1 with one CTA per SM, 11008 x 4096)
+    // (one token, 11008 x 4096: 9.9 us against 15.0 with a CTA that takes all of
+    // tensor memory)
     static constexpr int PER_SM = NB <= 64 ? 2 : 1;
     static constexpr int STAGES = NB <= 32 ? 4 : (NB <= 64 ? 3 : (NB <= 128 ? 5 : 4));
     static constexpr uint32_t TCOLS = PER_SM == 2 ? 256 : 512;
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(DF_THREADS, DfCfg<FMT, NB>::PER_SM) k_decode_f
             const int next = stage + 1 == S ? 0 : stage + 1;
             const uint32_t nphase = stage + 1 == S ? phase ^ 1 : phase;
             // test_wait: this stage's MMAs are ready and do not wait for the next's
-            // (8 tokens 4096 x 14336: 12.6 us against 13.5 with try_wait)
+            // (8 tokens 4096 x 14336 NV bf16: 12.6 us against 13.5 with try_wait)
             ready = kb + 1 < kb1 && mbar_test(&full[next], nphase);
             const int steps = min(4, (a.K - kb * DF_KB + 63) >> 6);
             const uint32_t sfa = tmem + NB + stage * P::SCOLS, sfb = sfa + 4 * C::SFT;

@@ -6,10 +6,12 @@
 //               up to HELD steps of the row stay in registers between the two
 //               uses, longer rows are read again (from L2).  One conversion
 //               and one product or division per value are the least that the
-//               definition allows, and issue slots (60 % taken) bound it with
-//               memory: 4096 x 14336 bf16 to NV 34.8 us, 3.8 TB/s of bytes
-//               read and written (floor 23 us); one token of 14336 4.2 us,
-//               which is the latency of load, row maximum and store.
+//               definition allows.  Load, maximum, conversions and store of a
+//               CTA follow one another, which 45 % occupancy covers in part:
+//               4096 x 14336 bf16 to NV 34.8 us, 3.8 TB/s of bytes read and
+//               written (floor 23 us), issue slots 60 % taken; one token of
+//               14336 4.2 us, which is the latency of load, row maximum and
+//               store.
 // k_dequant_fp4 16 output bytes per thread and step: 4096 x 14336 to bf16
 //               33.2 us, 4.5 TB/s (issue slots 66 % taken).
 #include <type_traits>

@@ -20,16 +20,16 @@
 //                   and the two overlap only in part (717 clocks together);
 //                   the stores leave the MMAs at 513.  An SM takes in about
 //                   53 bytes per clock, 38 KB per stage: 4096 x 14336 x 4096
-//                   NV runs in 96 us (5.0 PFLOP/s), 777 x 11008 x 4096 MX in
-//                   33 us, of which some 11 us are start, first loads and
-//                   epilogue.
+//                   NV runs in 100 us (4.8 PFLOP/s), 777 x 11008 x 4096 MX in
+//                   21.5 us (MMAs 11 us, operands 15 us), calls one after
+//                   another with cold operands.
 // k_gemm_fp4_few    few tokens: the weights are the M = 128 operand and the
 //                   tokens the N operand, so that every SM streams weights; K
 //                   is split over the CTAs of a cluster, whose sums are added
 //                   through distributed shared memory in rank order.  Bound
 //                   by latency (launch, first loads, exchange): 16 x 4096 x
-//                   4096 6.4 us, 512 x 1024 x 4096 7.9 us; by the weights
-//                   when they are many: 16 x 14336 x 14336 25.5 us (4.5 TB/s).
+//                   4096 6.3 us, 512 x 1024 x 4096 7.5 us; by the weights
+//                   when they are many: 16 x 14336 x 14336 24 us (4.8 TB/s).
 // No load uses cluster multicast.  Every mbarrier wait is bounded.
 #include "common.cuh"
 #include "fp4.cuh"
@@ -721,7 +721,7 @@ static cudaError_t launch_fp4_pair(const Fp4GemmArgs &a, cudaStream_t st)
 // with the most that fit).  fit[r] keeps each device's answer for r.
 // With two CTAs per SM the SMs' count decides: the answer counts one per SM,
 // and a cluster that is left over shares SMs (decode, one token, 11008 x 14336:
-// 19.7 us so, 26.9 by the answer).
+// 19.6 us so, 26.9 by the answer).
 template <typename Kernel>
 static int cluster_that_fits(Kernel kernel, cudaLaunchConfig_t cfg, int tiles, int per_sm, int k_blocks, DeviceAnswer (&fit)[9])
 {
@@ -790,12 +790,12 @@ static cudaError_t launch_fp4_t(const Fp4GemmArgs &a, cudaStream_t st)
     if (a.T <= 32) return launch_fp4_few<FMT, 32>(a, st);
     if (a.T <= 64) return launch_fp4_few<FMT, 64>(a, st);
     // One wave of 128 x 128 tiles at most: with K split over the SMs left and a
-    // short epilogue it beats 256 x 256 tiles at every length (512 x 1024 x 4096
-    // 7.9 against 16.9 us, 512 x 4096 x 14336 26.3 against 30.5, 128 x 14336 x
-    // 14336 33.8 against 37.8); with a second wave it loses (256 x 14336 x 4096
-    // 27.4 against 20.1, 768 x 4096 x 4096 25.3 against 18.2).
+    // short epilogue it beats 256 x 256 tiles at every length (tokens x outputs x
+    // K: 512 x 1024 x 4096 8.1 against 13.5 us, 512 x 4096 x 14336 24.3 against
+    // 25.9, 128 x 14336 x 14336 30.0 against 32.7); with a second wave it loses
+    // (256 x 14336 x 4096 22.3 against 16.1, 768 x 4096 x 4096 21.1 against 14.1).
     // At most 16, 32 or 64 tokens take narrower tiles: fewer bytes and MMAs
-    // (64 x 4096 x 4096 7.6 us as 64 columns, 9.0 as 128; 16 tokens 6.5).
+    // (64 x 4096 x 4096 7.4 us as 64 columns, 8.7 as 128; 16 tokens 6.3).
     if ((long long)((a.T + 127) / 128) * ((a.n_out + 127) / 128) <= sm_count()) return launch_fp4_few<FMT, 128>(a, st);
     return launch_fp4_pair<FMT>(a, st);
 }
